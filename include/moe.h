@@ -399,6 +399,150 @@ moe_status moe_aux_coef_update(const moe_stats* stats, float* coef, float beta, 
 moe_status moe_aux_coef_next(float coef, float drop_rate, float beta, float xi, float* next);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Around the layer: what a training step of a block built on it also needs.
+ * Layer norm (the layer's input is the norm of the residual stream), a balance
+ * loss per sequence with its gradient, and the optimiser's step.  The pages'
+ * figures for the layer are training figures (FastMoE announcement, "特色三";
+ * Skywork-MoE release, "训练Infra"); they give no formulas for these, and the
+ * usual ones are taken.  Pointers need the alignment of their element type
+ * only, workspaces 256 bytes; everything may be captured in a CUDA graph, and
+ * results do not depend on the order in which blocks run.
+ * ---------------------------------------------------------------------------
+ *
+ * Layer norm over the last axis of rows x d, contiguous rows.
+ *   0 <= rows, 1 <= d <= 16384 (else MOE_ERR_UNSUPPORTED), eps > 0.
+ *   *_dtype: MOE_DTYPE_F32 | BF16 | F16, each operand its own: x (and sum), y,
+ *   the weights gamma and beta, add, dy, dx (and dsum).  Arithmetic is fp32.
+ *
+ * moe_layer_norm_forward:
+ *     h = x, or x + add rounded to x_dtype (the residual addition: add is, for
+ *         one, the layer's fp32 out); mu, var = mean and population variance of h
+ *     y = (h - mu) / sqrt(var + eps) * gamma + beta
+ *   add[rows, d] or NULL; sum[rows, d] or NULL receives h (only with add; it
+ *   may be x itself); gamma[d], beta[d] or NULL (1, 0); mean[rows], rstd[rows]
+ *   fp32 or NULL receive mu and 1 / sqrt(var + eps).
+ * moe_layer_norm_backward: the gradients of <dy, y> + <dsum, h> with respect
+ *   to h (which are those of x and of add), gamma and beta.
+ *   dy[rows, d]; x[rows, d]: h of the forward (its sum when add was given);
+ *   mean, rstd: from the forward; gamma or NULL; dsum[rows, d] or NULL: the
+ *   gradient that reaches h past the norm; dx[rows, d] (may be dsum itself, or
+ *   dy when dy_dtype is dx_dtype); dgamma[d], dbeta[d] fp32 or NULL, fully written
+ *   (zeros when rows is 0), summed in a fixed order.
+ *   ws: moe_layer_norm_workspace_size(cfg) bytes; not read when dgamma and
+ *   dbeta are both NULL.
+ */
+typedef struct moe_norm_config {
+  int32_t rows, d;
+  float eps;
+  int32_t x_dtype, y_dtype, w_dtype, add_dtype, dy_dtype, dx_dtype;
+} moe_norm_config;
+
+size_t moe_layer_norm_workspace_size(const moe_norm_config* cfg);
+moe_status moe_layer_norm_forward(const moe_norm_config* cfg, const void* x, const void* add, const void* gamma,
+                                  const void* beta, void* y, void* sum, float* mean, float* rstd,
+                                  moe_stream_t stream);
+moe_status moe_layer_norm_backward(const moe_norm_config* cfg, const void* dy, const void* x, const float* mean,
+                                   const float* rstd, const void* gamma, const void* dsum, void* dx, float* dgamma,
+                                   float* dbeta, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Balance loss over the sequences of a batch, with per-expert counts and the
+ * gradient of the scores (the Switch form, as aux_loss of moe_stats, but per
+ * sequence, without padded tokens, and for softmax or sigmoid routers):
+ *   sequence s: the tokens t in [seq_offsets[s], seq_offsets[s+1]) with
+ *     mask[t] != 0, n_s of them; G: the sequences with n_s > 0
+ *   c_se = assignments of those tokens to expert e; f_se = E c_se / sum_e c_se
+ *     (0 when the sum is 0)
+ *   p_t = softmax(scores[t]), or sigmoid(scores[t]) / its sum over the experts
+ *   loss = (1/G) sum_s (1/n_s) sum_{t in s} sum_e f_se p_te     (0 when G = 0)
+ *   dscores = coef * dloss/dscores; the counts carry no gradient
+ *   T >= 0, 1 <= E <= 256, 1 <= k <= E, T*k <= 2^30, S >= 1 sequences,
+ *   S*E <= 2^30; score: MOE_SCORE_SOFTMAX | MOE_SCORE_SIGMOID; dtype: of scores
+ *   and dscores, MOE_DTYPE_F32 | MOE_DTYPE_BF16.
+ *   scores[T, E]: as moe_route_scores writes them, or another router's.  A
+ *     token whose scores are all -inf has no probabilities: it counts in n_s
+ *     and G, adds 0 to the loss and has gradient 0.  NaN and +inf (softmax)
+ *     give NaN; scores of tokens in no sequence or masked out are not read.
+ *   topk_idx[T, k] int32: the selected experts; counts[S, E] int32 is written.
+ *     An index outside [0, E) is not counted and sets MOE_DEV_BOUNDS.
+ *     NULL: counts is read instead, for counts that were added up over ranks or
+ *     batches after a call with scores, loss and dscores NULL (which counts
+ *     only); a sequence's sum must stay below 2^31.
+ *   seq_offsets[S+1] int32, non-decreasing inside [0, T] (else MOE_DEV_BOUNDS
+ *     and unspecified results), or NULL: one sequence of all T tokens (S = 1).
+ *   mask[T] uint8 or NULL (no padding).
+ *   coef: device fp32 scalar or NULL (1): moe_aux_coef_update's, for one.
+ *   loss: device fp32 scalar or NULL, not scaled by coef; dscores[T, E] or NULL,
+ *     fully written: 0 for tokens in no sequence or masked out.
+ *   stats: device moe_stats or NULL; only status is touched (bits OR-ed in).
+ *   ws: moe_balance_workspace_size(cfg) bytes.
+ */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+typedef struct moe_balance_config {
+  int32_t T, E, k, S;
+  int32_t score;
+  int32_t dtype;
+} moe_balance_config;
+
+size_t moe_balance_workspace_size(const moe_balance_config* cfg);
+moe_status moe_balance_loss(const moe_balance_config* cfg, const void* scores, const int32_t* topk_idx,
+                            const int32_t* seq_offsets, const uint8_t* mask, const float* coef, int32_t* counts,
+                            float* loss, void* dscores, moe_stats* stats, void* ws, size_t ws_bytes,
+                            moe_stream_t stream);
+
+/*
+ * One AdamW step over ntensors tensors in one launch (one more per 340
+ * tensors).  With g = grad * grad_scale, step number t = state->step + 1 and
+ * c_i = 1 - beta_i^t:
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr (m / c1) / (sqrt(v / c2) + eps)
+ * p is master where it is given (param is then p rounded), else param.
+ *   tensors: HOST array, read during the call; every pointer in it is a device
+ *     pointer.  A tensor is n >= 0 contiguous elements (0: skipped).
+ *     param[n] (param_dtype) and master[n] fp32 or NULL; grad[n] (grad_dtype);
+ *     dtypes MOE_DTYPE_F32 | BF16 | F16.
+ *     state_bits 32: m[n], v[n] fp32; m_scale, v_scale unused.
+ *     state_bits 8: m[n], v[n] bytes in blocks of MOE_ADAMW_BLOCK elements (the
+ *     last one may be short) with m_scale, v_scale fp32[ceil(n / block)]:
+ *       m = E4M3(m[i]) * m_scale[block],  sqrt(v) = E4M3(v[i]) * v_scale[block],
+ *     scale = max|.| / 448 over the block's finite values, at least
+ *     2^-100 / 448; codes round to nearest even; a root that is not 0 gets at
+ *     least the smallest code; a value that is not finite gets the NaN code.
+ *     The update itself uses the unrounded m and v.  A new state is zeros
+ *     throughout, for 32 and for 8 bits.
+ *   hyper (host): finite lr, 0 <= beta1, beta2 < 1, eps > 0.
+ *   lr: device fp32 scalar, used instead of hyper->lr, or NULL.
+ *   grad_scale: device fp32 scalar or NULL (1): gradient clipping, loss scaling.
+ *   state (device): step is advanced by one by the call, ticket is zero between
+ *     calls.  Start from zeros; a captured step replays as the next step.  Calls
+ *     that share a state must not overlap.
+ */
+#define MOE_ADAMW_BLOCK 256
+typedef struct moe_adamw_tensor {
+  void* param;
+  const void* grad;
+  float* master;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  int32_t param_dtype, grad_dtype, state_bits;
+  float weight_decay;
+} moe_adamw_tensor;
+typedef struct moe_adamw_hyper {
+  double lr, beta1, beta2, eps;
+} moe_adamw_hyper;
+typedef struct moe_adamw_state {
+  int32_t step;
+  uint32_t ticket;
+} moe_adamw_state;
+
+moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t ntensors, const moe_adamw_hyper* hyper,
+                          const float* lr, const float* grad_scale, moe_adamw_state* state, moe_stream_t stream);
+
+/*
  * Test hook for the failure path of the bounded waits.  No counterpart on the
  * pages.  Every wait inside the kernels gives up after a limit (2 s by
  * default), sets MOE_DEV_TIMEOUT in moe_stats.status, stops the kernel's other

@@ -9,6 +9,10 @@ CPU fallback: if the library is missing, loading it raises.
 Python names match the C entry points: ``moe_route``, ``moe_permute``,
 ``moe_expert_ffn``, ``moe_combine``, ``moe_layer_forward``, plus
 ``moe_scratch_size``, ``moe_workspace_size`` and ``moe_status_string``.
+Around the layer: ``moe_layer_norm_forward`` / ``_backward``,
+``moe_balance_loss`` and ``moe_adamw_step``; these also check that a tensor they
+are given is contiguous, of the configured type and size, and on the current
+device.
 """
 from __future__ import annotations
 
@@ -25,6 +29,10 @@ __all__ = [
     "moe_backward_workspace_size", "moe_layer_backward", "moe_mxfp8_weight_bytes", "moe_prepare_mxfp8_weights",
     "moe_workspace_size_mxfp8", "moe_layer_forward_mxfp8", "prepare_mxfp8", "moe_workspace_size_shared",
     "moe_layer_forward_shared",
+    "moe_norm_config", "make_norm_config", "moe_layer_norm_workspace_size", "moe_layer_norm_forward",
+    "moe_layer_norm_backward", "moe_balance_config", "make_balance_config", "moe_balance_workspace_size",
+    "moe_balance_loss", "moe_adamw_tensor", "moe_adamw_hyper", "adamw_tensor", "adamw_states", "AdamWPlan",
+    "make_adamw_plan", "moe_adamw_step", "MOE_ADAMW_BLOCK", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID",
     "read_stats", "STATS_BYTES", "MOE_ACT_RELU", "MOE_ACT_SWIGLU", "MOE_DTYPE_F32", "MOE_DTYPE_BF16",
     "MOE_DTYPE_F16", "MOE_DEV_TIMEOUT", "MOE_DEV_BOUNDS", "MOE_DEV_RANGE", "EXPORTED_SYMBOLS",
 ]
@@ -43,7 +51,10 @@ EXPORTED_SYMBOLS = ["moe_status_string", "moe_scratch_size", "moe_workspace_size
                     "moe_segments_scratch_size", "moe_expert_ffn_segments", "moe_backward_workspace_size",
                     "moe_layer_backward", "moe_mxfp8_weight_bytes", "moe_prepare_mxfp8_weights",
                     "moe_workspace_size_mxfp8", "moe_layer_forward_mxfp8", "moe_workspace_size_shared",
-                    "moe_layer_forward_shared"]
+                    "moe_layer_forward_shared", "moe_layer_norm_workspace_size", "moe_layer_norm_forward",
+                    "moe_layer_norm_backward", "moe_balance_workspace_size", "moe_balance_loss", "moe_adamw_step"]
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_ADAMW_BLOCK = 256
 MOE_STATIC_SCRATCH_BYTES = 2 << 20
 
 
@@ -66,9 +77,29 @@ class moe_ws_layout(ctypes.Structure):
                  "xp", "h", "yp", "scratch", "total"]]
 
 
+class moe_norm_config(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("d", ctypes.c_int32), ("eps", ctypes.c_float)] + [
+        (n, ctypes.c_int32) for n in ["x_dtype", "y_dtype", "w_dtype", "add_dtype", "dy_dtype", "dx_dtype"]]
+
+
+class moe_balance_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ["T", "E", "k", "S", "score", "dtype"]]
+
+
+class moe_adamw_tensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ["param", "grad", "master", "m", "v", "m_scale", "v_scale"]] + [
+        ("n", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+        ("state_bits", ctypes.c_int32), ("weight_decay", ctypes.c_float)]
+
+
+class moe_adamw_hyper(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ["lr", "beta1", "beta2", "eps"]]
+
+
 class MoeError(RuntimeError):
-    def __init__(self, fn: str, code: int):
-        super().__init__(f"{fn} failed: {STATUS_NAMES.get(code, code)} ({moe_status_string(code)})")
+    def __init__(self, fn: str, code: int, why: str = ""):
+        super().__init__(f"{fn} failed: {STATUS_NAMES.get(code, code)} ({moe_status_string(code)})"
+                         + (f": {why}" if why else ""))
         self.code = code
 
 
@@ -122,10 +153,20 @@ def lib() -> ctypes.CDLL:
     L.moe_backward_workspace_size.restype = ctypes.c_size_t
     L.moe_layer_backward.argtypes = [cfgp, P, P, P, P, P, P, f32, f32, P, ctypes.c_size_t, P, P, P, P, P, P, P, P,
                                      ctypes.c_size_t, P]
+    normp, balp = ctypes.POINTER(moe_norm_config), ctypes.POINTER(moe_balance_config)
+    L.moe_layer_norm_workspace_size.argtypes = [normp]
+    L.moe_layer_norm_workspace_size.restype = ctypes.c_size_t
+    L.moe_layer_norm_forward.argtypes = [normp] + [P] * 9
+    L.moe_layer_norm_backward.argtypes = [normp] + [P] * 10 + [ctypes.c_size_t, P]
+    L.moe_balance_workspace_size.argtypes = [balp]
+    L.moe_balance_workspace_size.restype = ctypes.c_size_t
+    L.moe_balance_loss.argtypes = [balp] + [P] * 10 + [ctypes.c_size_t, P]
+    L.moe_adamw_step.argtypes = [ctypes.POINTER(moe_adamw_tensor), i32, ctypes.POINTER(moe_adamw_hyper), P, P, P, P]
     for n in ["moe_route", "moe_permute", "moe_expert_ffn", "moe_combine", "moe_layer_forward",
               "moe_convert_bf16_to_f16", "moe_permute_static", "moe_expert_ffn_combine", "moe_aux_coef_update",
               "moe_aux_coef_next", "moe_testing_set_expert_wait", "moe_expert_ffn_segments", "moe_layer_backward",
-              "moe_prepare_mxfp8_weights", "moe_layer_forward_mxfp8", "moe_layer_forward_shared"]:
+              "moe_prepare_mxfp8_weights", "moe_layer_forward_mxfp8", "moe_layer_forward_shared",
+              "moe_layer_norm_forward", "moe_layer_norm_backward", "moe_balance_loss", "moe_adamw_step"]:
         getattr(L, n).restype = st
     _lib = L
     return L
@@ -347,6 +388,190 @@ def prepare_w2(cfg: moe_config, w2):
     out = torch.empty(w2.shape, dtype=torch.float16, device=w2.device)
     moe_convert_bf16_to_f16(w2, out)
     return out
+
+
+# ------------------------------------------------------------ around the layer
+_TORCH_DTYPES = None
+
+
+def _torch_dtype(code: int):
+    global _TORCH_DTYPES
+    if _TORCH_DTYPES is None:
+        import torch
+        _TORCH_DTYPES = {MOE_DTYPE_F32: torch.float32, MOE_DTYPE_BF16: torch.bfloat16, MOE_DTYPE_F16: torch.float16}
+    return _TORCH_DTYPES.get(code)
+
+
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_available() else -2   # -1 is what a CPU tensor says
+
+
+def _arg(fn: str, name: str, t, dev: int, dtype, n: int) -> Optional[int]:
+    """Device pointer of an operand of n contiguous elements of dtype (None and
+    raw ints pass as they are); anything else is refused before it is read."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.get_device() != dev:
+        raise MoeError(fn, 1, f"{name} is on {t.device}, not on the current CUDA device")
+    if t.dtype != dtype:
+        raise MoeError(fn, 1, f"{name} is {t.dtype}, not {dtype}")
+    if t.numel() != n:
+        raise MoeError(fn, 1, f"{name} has {t.numel()} elements, not {n}")
+    if not t.is_contiguous():
+        raise MoeError(fn, 1, f"{name} is not contiguous")
+    return t.data_ptr()
+
+
+def _workspace(fn: str, ws, dev: int):
+    """(pointer, bytes) of a workspace tensor (None: no workspace)."""
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise MoeError(fn, 3, "ws is not a contiguous tensor on the current CUDA device")
+    return ws.data_ptr(), _nbytes(ws)
+
+
+def make_norm_config(rows: int, d: int, eps: float = 1e-5, x: str = "bf16", y: Optional[str] = None, w: str = "f32",
+                     add: Optional[str] = None, dy: Optional[str] = None, dx: Optional[str] = None) -> moe_norm_config:
+    """Types of the operands ("f32", "bf16", "f16"): y and dx follow x unless
+    given; add and dy are fp32 unless given (the layer's out, and its dx)."""
+    return moe_norm_config(rows, d, eps, _DTYPES[x], _DTYPES[y or x], _DTYPES[w], _DTYPES[add or "f32"],
+                           _DTYPES[dy or "f32"], _DTYPES[dx or x])
+
+
+def moe_layer_norm_workspace_size(cfg: moe_norm_config) -> int:
+    return lib().moe_layer_norm_workspace_size(ctypes.byref(cfg))
+
+
+def moe_layer_norm_forward(cfg, x, gamma, beta, y, add=None, sum=None, mean=None, rstd=None, stream=None):
+    """y = norm(x) * gamma + beta, or of x + add, which sum receives; mean and
+    rstd (fp32, one per row) are what the backward takes."""
+    fn, dev, n = "moe_layer_norm_forward", _current_device(), cfg.rows * cfg.d
+    xt, wt, f32 = _torch_dtype(cfg.x_dtype), _torch_dtype(cfg.w_dtype), _torch_dtype(MOE_DTYPE_F32)
+    _check(fn, lib().moe_layer_norm_forward(
+        ctypes.byref(cfg), _arg(fn, "x", x, dev, xt, n), _arg(fn, "add", add, dev, _torch_dtype(cfg.add_dtype), n),
+        _arg(fn, "gamma", gamma, dev, wt, cfg.d), _arg(fn, "beta", beta, dev, wt, cfg.d),
+        _arg(fn, "y", y, dev, _torch_dtype(cfg.y_dtype), n), _arg(fn, "sum", sum, dev, xt, n),
+        _arg(fn, "mean", mean, dev, f32, cfg.rows), _arg(fn, "rstd", rstd, dev, f32, cfg.rows), _stream(stream)))
+
+
+def moe_layer_norm_backward(cfg, dy, x, mean, rstd, gamma, dx, dgamma=None, dbeta=None, ws=None, dsum=None,
+                            stream=None):
+    """dx (of what the forward normalised; dsum is added to it), dgamma, dbeta."""
+    fn, dev, n = "moe_layer_norm_backward", _current_device(), cfg.rows * cfg.d
+    dxt, f32 = _torch_dtype(cfg.dx_dtype), _torch_dtype(MOE_DTYPE_F32)
+    wp, wn = _workspace(fn, ws, dev)
+    _check(fn, lib().moe_layer_norm_backward(
+        ctypes.byref(cfg), _arg(fn, "dy", dy, dev, _torch_dtype(cfg.dy_dtype), n),
+        _arg(fn, "x", x, dev, _torch_dtype(cfg.x_dtype), n), _arg(fn, "mean", mean, dev, f32, cfg.rows),
+        _arg(fn, "rstd", rstd, dev, f32, cfg.rows), _arg(fn, "gamma", gamma, dev, _torch_dtype(cfg.w_dtype), cfg.d),
+        _arg(fn, "dsum", dsum, dev, dxt, n), _arg(fn, "dx", dx, dev, dxt, n),
+        _arg(fn, "dgamma", dgamma, dev, f32, cfg.d), _arg(fn, "dbeta", dbeta, dev, f32, cfg.d), wp, wn,
+        _stream(stream)))
+
+
+def make_balance_config(T: int, E: int, k: int, S: int = 1, score: str = "softmax",
+                        dtype: str = "f32") -> moe_balance_config:
+    """score: "softmax" or "sigmoid" (normalised over the experts); dtype: of the scores."""
+    return moe_balance_config(T, E, k, S, {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}[score],
+                              _DTYPES[dtype])
+
+
+def moe_balance_workspace_size(cfg: moe_balance_config) -> int:
+    return lib().moe_balance_workspace_size(ctypes.byref(cfg))
+
+
+def moe_balance_loss(cfg, scores, topk_idx, counts, loss, ws, seq_offsets=None, mask=None, coef=None, dscores=None,
+                     stats=None, stream=None):
+    """Balance loss, per-expert counts and coef * dloss/dscores (see
+    include/moe.h).  topk_idx None: counts is read; scores, loss and dscores
+    None: only counts."""
+    import torch
+    fn, dev, n = "moe_balance_loss", _current_device(), cfg.T * cfg.E
+    zt, f32, i32 = _torch_dtype(cfg.dtype), torch.float32, torch.int32
+    cp = _arg(fn, "counts", counts, dev, i32, cfg.S * cfg.E)
+    ip = _arg(fn, "topk_idx", topk_idx, dev, i32, cfg.T * cfg.k)
+    if topk_idx is not None and cfg.T == 0:
+        ip = cp   # an empty tensor has no address: any other than NULL says that counts is written
+    if mask is not None and not isinstance(mask, int) and mask.dtype == torch.bool:
+        mask = mask.view(torch.uint8)
+    wp, wn = _workspace(fn, ws, dev)
+    _check(fn, lib().moe_balance_loss(
+        ctypes.byref(cfg), _arg(fn, "scores", scores, dev, zt, n), ip,
+        _arg(fn, "seq_offsets", seq_offsets, dev, i32, cfg.S + 1), _arg(fn, "mask", mask, dev, torch.uint8, cfg.T),
+        _arg(fn, "coef", coef, dev, f32, 1), cp, _arg(fn, "loss", loss, dev, f32, 1),
+        _arg(fn, "dscores", dscores, dev, zt, n), _arg(fn, "stats", stats, dev, torch.uint8, STATS_BYTES), wp, wn,
+        _stream(stream)))
+
+
+def adamw_states(param, bits: int = 32):
+    """New optimiser states of a tensor: (m, v, m_scale, v_scale), zeros; the scales are None for 32 bits."""
+    import torch
+    n = param.numel()
+    if bits == 32:
+        return (torch.zeros(n, device=param.device), torch.zeros(n, device=param.device), None, None)
+    blocks = (n + MOE_ADAMW_BLOCK - 1) // MOE_ADAMW_BLOCK
+    return tuple(torch.zeros(n, dtype=torch.float8_e4m3fn, device=param.device) for _ in range(2)) + tuple(
+        torch.zeros(blocks, device=param.device) for _ in range(2))
+
+
+def adamw_tensor(param, grad, m, v, m_scale=None, v_scale=None, master=None, weight_decay: float = 0.0) -> dict:
+    """One tensor of an AdamW plan.  fp32 m and v: 32-bit states; float8_e4m3fn
+    (or uint8) ones with their scales: 8-bit states."""
+    return dict(param=param, grad=grad, m=m, v=v, m_scale=m_scale, v_scale=v_scale, master=master,
+                weight_decay=weight_decay)
+
+
+class AdamWPlan:
+    """The tensors and constants of an optimiser, laid out once for
+    moe_adamw_step.  It keeps the tensors alive; their contents (the gradients
+    above all) are read at each step."""
+
+    def __init__(self, tensors, lr: float, beta1: float, beta2: float, eps: float):
+        import torch
+        fn, dev = "make_adamw_plan", _current_device()
+        codes = {v: k for k, v in ((c, _torch_dtype(c)) for c in (MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_F16))}
+        self.tensors = [dict(t) for t in tensors]
+        self.device = dev
+        self.hyper = moe_adamw_hyper(lr, beta1, beta2, eps)
+        self.table = (moe_adamw_tensor * len(self.tensors))()
+        for i, t in enumerate(self.tensors):
+            n = t["param"].numel()
+            eight = t["m"].dtype != torch.float32
+            if t["param"].dtype not in codes or t["grad"].dtype not in codes:
+                raise MoeError(fn, 1, f"tensor {i}: param and grad are float32, bfloat16 or float16")
+            if eight and (t["m"].dtype not in (torch.float8_e4m3fn, torch.uint8)
+                          or t["m_scale"] is None or t["v_scale"] is None):
+                raise MoeError(fn, 1, f"tensor {i}: 8-bit m and v are float8_e4m3fn or uint8, with scales")
+            nb = (n + MOE_ADAMW_BLOCK - 1) // MOE_ADAMW_BLOCK
+            e = self.table[i]
+            for name, dtype, count in (("param", t["param"].dtype, n), ("grad", t["grad"].dtype, n),
+                                       ("master", torch.float32, n), ("m", t["m"].dtype, n), ("v", t["m"].dtype, n),
+                                       ("m_scale", torch.float32, nb), ("v_scale", torch.float32, nb)):
+                setattr(e, name, _arg(fn, f"tensor {i}: {name}", t[name], dev, dtype, count))
+            e.n, e.state_bits, e.weight_decay = n, 8 if eight else 32, t["weight_decay"]
+            e.param_dtype, e.grad_dtype = codes[t["param"].dtype], codes[t["grad"].dtype]
+
+
+def make_adamw_plan(tensors, lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999,
+                    eps: float = 1e-8) -> AdamWPlan:
+    """tensors: adamw_tensor(...)s.  plan.hyper may be changed between steps."""
+    return AdamWPlan(tensors, lr, beta1, beta2, eps)
+
+
+def moe_adamw_step(plan: AdamWPlan, state, lr=None, grad_scale=None, stream=None):
+    """One step over the plan's tensors.  state: int32[2] device tensor, zeros
+    before the first step (state[0] counts the steps).  lr, grad_scale: device
+    fp32 scalars or None (plan.hyper.lr, 1)."""
+    import torch
+    fn, dev = "moe_adamw_step", _current_device()
+    if plan.device != dev:
+        raise MoeError(fn, 1, f"the plan's tensors are on cuda:{plan.device}, not on the current CUDA device")
+    _check(fn, lib().moe_adamw_step(plan.table, len(plan.table), ctypes.byref(plan.hyper),
+                                    _arg(fn, "lr", lr, dev, torch.float32, 1),
+                                    _arg(fn, "grad_scale", grad_scale, dev, torch.float32, 1),
+                                    _arg(fn, "state", state, dev, torch.int32, 2), _stream(stream)))
 
 
 def read_stats(stats_tensor) -> dict:

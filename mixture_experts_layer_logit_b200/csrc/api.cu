@@ -315,6 +315,43 @@ SharedLayout shared_layout(const moe_config& c, int Fs) {
   return L;
 }
 
+bool any_dtype(int32_t dt) { return dt == MOE_DTYPE_F32 || dt == MOE_DTYPE_BF16 || dt == MOE_DTYPE_F16; }
+
+// a pointer aligned to its element type (NULL passes)
+bool aligned_to(const void* p, int32_t dt) {
+  return (reinterpret_cast<uintptr_t>(p) & (dt == MOE_DTYPE_F32 ? 3u : 1u)) == 0;
+}
+
+moe_status check_norm(const moe_norm_config* c) {
+  if (c == nullptr || c->rows < 0 || c->d < 1 || !isfinite(c->eps) || !(c->eps > 0.f)) return MOE_ERR_ARG;
+  for (int32_t dt : {c->x_dtype, c->y_dtype, c->w_dtype, c->add_dtype, c->dy_dtype, c->dx_dtype})
+    if (!any_dtype(dt)) return MOE_ERR_ARG;
+  if (c->d > 16384) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_balance(const moe_balance_config* c) {
+  if (c == nullptr || c->T < 0 || c->E < 1 || c->k < 1 || c->k > c->E || c->S < 1) return MOE_ERR_ARG;
+  if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) return MOE_ERR_ARG;
+  if (c->dtype != MOE_DTYPE_F32 && c->dtype != MOE_DTYPE_BF16) return MOE_ERR_ARG;
+  if (c->E > kMaxExperts || (long long)c->T * c->k > (1LL << 30) || (long long)c->S * c->E > (1LL << 30))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_adamw(const moe_adamw_tensor& t) {
+  if (t.n < 0) return MOE_ERR_ARG;
+  if (!any_dtype(t.param_dtype) || !any_dtype(t.grad_dtype) || !isfinite(t.weight_decay)) return MOE_ERR_ARG;
+  if (t.state_bits != 8 && t.state_bits != 32) return MOE_ERR_ARG;
+  if (t.n == 0) return MOE_OK;
+  if (t.param == nullptr || t.grad == nullptr || t.m == nullptr || t.v == nullptr) return MOE_ERR_ARG;
+  if (!aligned_to(t.param, t.param_dtype) || !aligned_to(t.grad, t.grad_dtype) || !aligned4(t.master))
+    return MOE_ERR_ARG;
+  if (t.state_bits == 32) return aligned4(t.m) && aligned4(t.v) ? MOE_OK : MOE_ERR_ARG;
+  return t.m_scale != nullptr && t.v_scale != nullptr && aligned4(t.m_scale) && aligned4(t.v_scale) ? MOE_OK
+                                                                                                    : MOE_ERR_ARG;
+}
+
 }  // namespace
 
 extern "C" {
@@ -564,6 +601,97 @@ moe_status moe_aux_coef_next(float coef, float drop_rate, float beta, float xi, 
   if (!(beta >= 0.f && beta <= 1.f) || !(xi >= 0.f) || !isfinite(xi)) return MOE_ERR_ARG;
   *next = aux_coef_step(coef, drop_rate, beta, xi);
   return MOE_OK;
+}
+
+size_t moe_layer_norm_workspace_size(const moe_norm_config* cfg) {
+  if (check_norm(cfg) != MOE_OK) return 0;
+  return align256(sizeof(float) * 2 * (size_t)cfg->d * norm_bwd_blocks(*cfg));
+}
+
+moe_status moe_layer_norm_forward(const moe_norm_config* cfg, const void* x, const void* add, const void* gamma,
+                                  const void* beta, void* y, void* sum, float* mean, float* rstd,
+                                  moe_stream_t stream) {
+  moe_status st = check_norm(cfg);
+  if (st != MOE_OK) return st;
+  const moe_norm_config& c = *cfg;
+  if (c.rows > 0 && (x == nullptr || y == nullptr)) return MOE_ERR_ARG;
+  if (sum != nullptr && add == nullptr) return MOE_ERR_ARG;
+  if (!aligned_to(x, c.x_dtype) || !aligned_to(add, c.add_dtype) || !aligned_to(gamma, c.w_dtype) ||
+      !aligned_to(beta, c.w_dtype) || !aligned_to(y, c.y_dtype) || !aligned_to(sum, c.x_dtype) || !aligned4(mean) ||
+      !aligned4(rstd))
+    return MOE_ERR_ARG;
+  if (c.rows == 0) return MOE_OK;
+  if ((st = check_device(true)) != MOE_OK) return st;
+  return cuda_status(launch_norm_fwd(c, x, add, gamma, beta, y, sum, mean, rstd,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_layer_norm_backward(const moe_norm_config* cfg, const void* dy, const void* x, const float* mean,
+                                   const float* rstd, const void* gamma, const void* dsum, void* dx, float* dgamma,
+                                   float* dbeta, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  moe_status st = check_norm(cfg);
+  if (st != MOE_OK) return st;
+  const moe_norm_config& c = *cfg;
+  if (c.rows > 0 && (dy == nullptr || x == nullptr || mean == nullptr || rstd == nullptr || dx == nullptr))
+    return MOE_ERR_ARG;
+  if (!aligned_to(dy, c.dy_dtype) || !aligned_to(x, c.x_dtype) || !aligned4(mean) || !aligned4(rstd) ||
+      !aligned_to(gamma, c.w_dtype) || !aligned_to(dsum, c.dx_dtype) || !aligned_to(dx, c.dx_dtype) ||
+      !aligned4(dgamma) || !aligned4(dbeta))
+    return MOE_ERR_ARG;
+  const bool weights = dgamma != nullptr || dbeta != nullptr;
+  if (weights && (st = check_ws(ws, ws_bytes, moe_layer_norm_workspace_size(cfg))) != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (c.rows == 0 && !weights) return MOE_OK;
+  if ((st = check_device(true)) != MOE_OK) return st;
+  if (c.rows == 0) {   // no row: the weights' gradient is zero
+    for (float* p : {dgamma, dbeta})
+      if (p != nullptr && cudaMemsetAsync(p, 0, sizeof(float) * (size_t)c.d, s) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  return cuda_status(launch_norm_bwd(c, dy, x, mean, rstd, gamma, dsum, dx, dgamma, dbeta, static_cast<float*>(ws),
+                                     s));
+}
+
+size_t moe_balance_workspace_size(const moe_balance_config* cfg) {
+  if (check_balance(cfg) != MOE_OK) return 0;
+  return balance_layout(*cfg).total;
+}
+
+moe_status moe_balance_loss(const moe_balance_config* cfg, const void* scores, const int32_t* topk_idx,
+                            const int32_t* seq_offsets, const uint8_t* mask, const float* coef, int32_t* counts,
+                            float* loss, void* dscores, moe_stats* stats, void* ws, size_t ws_bytes,
+                            moe_stream_t stream) {
+  moe_status st = check_balance(cfg);
+  if (st != MOE_OK) return st;
+  const moe_balance_config& c = *cfg;
+  const bool graded = loss != nullptr || dscores != nullptr;
+  if (counts == nullptr || (c.S != 1 && seq_offsets == nullptr)) return MOE_ERR_ARG;
+  // scores without an output, an output without scores, or nothing to do at all
+  if (c.T > 0 && (scores != nullptr) != graded) return MOE_ERR_ARG;
+  if (c.T > 0 && topk_idx == nullptr && !graded) return MOE_ERR_ARG;
+  if (!aligned_to(scores, c.dtype) || !aligned4(topk_idx) || !aligned4(seq_offsets) || !aligned4(coef) ||
+      !aligned4(counts) || !aligned4(loss) || !aligned_to(dscores, c.dtype) || !aligned4(stats))
+    return MOE_ERR_ARG;
+  if ((st = check_ws(ws, ws_bytes, balance_layout(c).total)) != MOE_OK) return st;
+  if ((st = check_device(true)) != MOE_OK) return st;
+  return cuda_status(launch_balance(c, scores, topk_idx, seq_offsets, mask, coef, counts, loss, dscores, stats, ws,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t ntensors, const moe_adamw_hyper* hyper,
+                          const float* lr, const float* grad_scale, moe_adamw_state* state, moe_stream_t stream) {
+  if (ntensors < 0 || (ntensors > 0 && tensors == nullptr) || hyper == nullptr || state == nullptr)
+    return MOE_ERR_ARG;
+  if (!isfinite(hyper->lr) || !(hyper->beta1 >= 0.0 && hyper->beta1 < 1.0) ||
+      !(hyper->beta2 >= 0.0 && hyper->beta2 < 1.0) || !isfinite(hyper->eps) || !((float)hyper->eps > 0.f))
+    return MOE_ERR_ARG;
+  if (!aligned4(lr) || !aligned4(grad_scale) || !aligned4(state)) return MOE_ERR_ARG;
+  moe_status st;
+  for (int32_t i = 0; i < ntensors; ++i)
+    if ((st = check_adamw(tensors[i])) != MOE_OK) return st;
+  if ((st = check_device(true)) != MOE_OK) return st;
+  return cuda_status(launch_adamw(tensors, ntensors, *hyper, lr, grad_scale, state,
+                                  reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_segments_scratch_size(const moe_config* cfg, int32_t nseg, int32_t rows) {

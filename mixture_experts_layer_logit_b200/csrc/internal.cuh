@@ -206,6 +206,27 @@ cudaError_t launch_mx_experts(const moe_config& c, const MxBuffers& b, const voi
 cudaError_t launch_combine(const moe_config& c, const void* yp, const int32_t* row_of,
                            const float* topk_w, void* out, cudaStream_t s);
 
+// ------------------------------------------------------- around the layer
+// Blocks of the layer norm's backward; each leaves [2][d] floats in `part`.
+int norm_bwd_blocks(const moe_norm_config& c);
+cudaError_t launch_norm_fwd(const moe_norm_config& c, const void* x, const void* add, const void* gamma,
+                            const void* beta, void* y, void* sum, float* mean, float* rstd, cudaStream_t s);
+cudaError_t launch_norm_bwd(const moe_norm_config& c, const void* dy, const void* x, const float* mean,
+                            const float* rstd, const void* gamma, const void* dsum, void* dx, float* dgamma,
+                            float* dbeta, float* part, cudaStream_t s);
+
+// Byte offsets in the balance loss's workspace: [0, part) is zeroed by the call.
+struct BalanceLayout {
+  size_t nkept, part, total;
+};
+BalanceLayout balance_layout(const moe_balance_config& c);
+cudaError_t launch_balance(const moe_balance_config& c, const void* scores, const int32_t* topk, const int32_t* off,
+                           const unsigned char* mask, const float* coef, int32_t* counts, float* loss, void* dscores,
+                           moe_stats* stats, void* ws, cudaStream_t s);
+
+cudaError_t launch_adamw(const moe_adamw_tensor* t, int nt, const moe_adamw_hyper& hy, const float* lr_dev,
+                         const float* grad_scale, moe_adamw_state* state, cudaStream_t s);
+
 // One step of the layer-wise adaptive aux-loss coefficient (Skywork-MoE
 // release, "2.自适应的Aux Loss"): an exponential moving average, smoothing
 // beta, of xi times the drop rate.  The same expression on host and device.
