@@ -447,6 +447,28 @@ moe_status moe_layer_norm_backward(const moe_norm_config* cfg, const void* dy, c
                                    float* dbeta, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
+ * The layer with its router's scores in the open, for a loss on them:
+ * moe_route, moe_layer_forward and moe_layer_backward with one more argument
+ * each (NULL: exactly those calls).
+ *   scores[T, E] fp32 or NULL receives the scores that the softmax takes (z_hat
+ *     when lambda > 0, else z with its bias), whatever the capacity drops.
+ *   dscores[T, E] fp32 or NULL: a gradient with respect to those scores, such
+ *     as moe_balance_loss's, added to the one that comes from out, the aux
+ *     loss and the z-loss before it goes on to dx, dWg and dbg.
+ */
+moe_status moe_route_scores(const moe_config* cfg, const void* x, const void* Wg, const float* bg,
+                            int32_t* topk_idx, float* topk_w, float* gap, float* prob_mean, float* z_loss,
+                            float* scores, void* ws, size_t ws_bytes, moe_stream_t stream);
+moe_status moe_layer_forward_scores(const moe_config* cfg, const void* x, const void* Wg, const float* bg,
+                                    const void* W1, const void* W2, void* out, moe_stats* stats, float* scores,
+                                    void* ws, size_t ws_bytes, moe_stream_t stream);
+moe_status moe_layer_backward_scores(const moe_config* cfg, const void* x, const void* Wg, const float* bg,
+                                     const void* W1, const void* W2, const float* dout, const float* dscores,
+                                     float aux_coef, float z_coef, const void* fws, size_t fws_bytes, float* dx,
+                                     float* dWg, float* dbg, float* dW1, float* dW2, float* dw, moe_stats* stats,
+                                     void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
  * Balance loss over the sequences of a batch, with per-expert counts and the
  * gradient of the scores (the Switch form, as aux_loss of moe_stats, but per
  * sequence, without padded tokens, and for softmax or sigmoid routers):

@@ -29,6 +29,7 @@ __all__ = [
     "moe_backward_workspace_size", "moe_layer_backward", "moe_mxfp8_weight_bytes", "moe_prepare_mxfp8_weights",
     "moe_workspace_size_mxfp8", "moe_layer_forward_mxfp8", "prepare_mxfp8", "moe_workspace_size_shared",
     "moe_layer_forward_shared",
+    "moe_route_scores", "moe_layer_forward_scores", "moe_layer_backward_scores",
     "moe_norm_config", "make_norm_config", "moe_layer_norm_workspace_size", "moe_layer_norm_forward",
     "moe_layer_norm_backward", "moe_balance_config", "make_balance_config", "moe_balance_workspace_size",
     "moe_balance_loss", "moe_adamw_tensor", "moe_adamw_hyper", "adamw_tensor", "adamw_states", "AdamWPlan",
@@ -52,7 +53,8 @@ EXPORTED_SYMBOLS = ["moe_status_string", "moe_scratch_size", "moe_workspace_size
                     "moe_layer_backward", "moe_mxfp8_weight_bytes", "moe_prepare_mxfp8_weights",
                     "moe_workspace_size_mxfp8", "moe_layer_forward_mxfp8", "moe_workspace_size_shared",
                     "moe_layer_forward_shared", "moe_layer_norm_workspace_size", "moe_layer_norm_forward",
-                    "moe_layer_norm_backward", "moe_balance_workspace_size", "moe_balance_loss", "moe_adamw_step"]
+                    "moe_layer_norm_backward", "moe_route_scores", "moe_layer_forward_scores",
+                    "moe_layer_backward_scores", "moe_balance_workspace_size", "moe_balance_loss", "moe_adamw_step"]
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_ADAMW_BLOCK = 256
 MOE_STATIC_SCRATCH_BYTES = 2 << 20
@@ -158,6 +160,10 @@ def lib() -> ctypes.CDLL:
     L.moe_layer_norm_workspace_size.restype = ctypes.c_size_t
     L.moe_layer_norm_forward.argtypes = [normp] + [P] * 9
     L.moe_layer_norm_backward.argtypes = [normp] + [P] * 10 + [ctypes.c_size_t, P]
+    L.moe_route_scores.argtypes = [cfgp, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    L.moe_layer_forward_scores.argtypes = [cfgp, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    L.moe_layer_backward_scores.argtypes = [cfgp, P, P, P, P, P, P, P, f32, f32, P, ctypes.c_size_t, P, P, P, P, P, P,
+                                            P, P, ctypes.c_size_t, P]
     L.moe_balance_workspace_size.argtypes = [balp]
     L.moe_balance_workspace_size.restype = ctypes.c_size_t
     L.moe_balance_loss.argtypes = [balp] + [P] * 10 + [ctypes.c_size_t, P]
@@ -166,7 +172,8 @@ def lib() -> ctypes.CDLL:
               "moe_convert_bf16_to_f16", "moe_permute_static", "moe_expert_ffn_combine", "moe_aux_coef_update",
               "moe_aux_coef_next", "moe_testing_set_expert_wait", "moe_expert_ffn_segments", "moe_layer_backward",
               "moe_prepare_mxfp8_weights", "moe_layer_forward_mxfp8", "moe_layer_forward_shared",
-              "moe_layer_norm_forward", "moe_layer_norm_backward", "moe_balance_loss", "moe_adamw_step"]:
+              "moe_layer_norm_forward", "moe_layer_norm_backward", "moe_route_scores", "moe_layer_forward_scores",
+              "moe_layer_backward_scores", "moe_balance_loss", "moe_adamw_step"]:
         getattr(L, n).restype = st
     _lib = L
     return L
@@ -471,6 +478,35 @@ def moe_layer_norm_backward(cfg, dy, x, mean, rstd, gamma, dx, dgamma=None, dbet
         _stream(stream)))
 
 
+def moe_route_scores(cfg, x, Wg, bg, topk_idx, topk_w, gap, prob_mean, scores, ws, stream=None, z_loss=None):
+    """moe_route that also writes the scores the softmax takes (fp32 [T, E])."""
+    fn = "moe_route_scores"
+    sp = _arg(fn, "scores", scores, _current_device(), _torch_dtype(MOE_DTYPE_F32), cfg.T * cfg.E)
+    _check(fn, lib().moe_route_scores(ctypes.byref(cfg), _ptr(x), _ptr(Wg), _ptr(bg), _ptr(topk_idx), _ptr(topk_w),
+                                      _ptr(gap), _ptr(prob_mean), _ptr(z_loss), sp, _ptr(ws), _nbytes(ws),
+                                      _stream(stream)))
+
+
+def moe_layer_forward_scores(cfg, x, Wg, bg, W1, W2, out, stats, scores, ws, stream=None):
+    """moe_layer_forward that also writes the router's scores (fp32 [T, E])."""
+    fn = "moe_layer_forward_scores"
+    sp = _arg(fn, "scores", scores, _current_device(), _torch_dtype(MOE_DTYPE_F32), cfg.T * cfg.E)
+    _check(fn, lib().moe_layer_forward_scores(ctypes.byref(cfg), _ptr(x), _ptr(Wg), _ptr(bg), _ptr(W1), _ptr(W2),
+                                              _ptr(out), _ptr(stats), sp, _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_layer_backward_scores(cfg, x, Wg, bg, W1, W2, dout, dscores, aux_coef, z_coef, fws, dx, dWg, dbg, dW1, dW2,
+                              dw, stats, ws, stream=None):
+    """moe_layer_backward with a gradient of the scores (fp32 [T, E], e.g.
+    moe_balance_loss's dscores) added on its way to dx, dWg and dbg."""
+    fn = "moe_layer_backward_scores"
+    sp = _arg(fn, "dscores", dscores, _current_device(), _torch_dtype(MOE_DTYPE_F32), cfg.T * cfg.E)
+    _check(fn, lib().moe_layer_backward_scores(
+        ctypes.byref(cfg), _ptr(x), _ptr(Wg), _ptr(bg), _ptr(W1), _ptr(W2), _ptr(dout), sp, aux_coef, z_coef,
+        _ptr(fws), _nbytes(fws), _ptr(dx), _ptr(dWg), _ptr(dbg), _ptr(dW1), _ptr(dW2), _ptr(dw), _ptr(stats),
+        _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
 def make_balance_config(T: int, E: int, k: int, S: int = 1, score: str = "softmax",
                         dtype: str = "f32") -> moe_balance_config:
     """score: "softmax" or "sigmoid" (normalised over the experts); dtype: of the scores."""
@@ -509,6 +545,8 @@ def adamw_states(param, bits: int = 32):
     """New optimiser states of a tensor: (m, v, m_scale, v_scale), zeros; the scales are None for 32 bits."""
     import torch
     n = param.numel()
+    if bits not in (8, 32):
+        raise ValueError(f"states have 8 or 32 bits, not {bits}")
     if bits == 32:
         return (torch.zeros(n, device=param.device), torch.zeros(n, device=param.device), None, None)
     blocks = (n + MOE_ADAMW_BLOCK - 1) // MOE_ADAMW_BLOCK

@@ -382,13 +382,19 @@ size_t moe_workspace_size(const moe_config* cfg, moe_ws_layout* layout) {
 moe_status moe_route(const moe_config* cfg, const void* x, const void* Wg, const float* bg,
                      int32_t* topk_idx, float* topk_w, float* gap, float* prob_mean, float* z_loss,
                      void* ws, size_t ws_bytes, moe_stream_t stream) {
+  return moe_route_scores(cfg, x, Wg, bg, topk_idx, topk_w, gap, prob_mean, z_loss, nullptr, ws, ws_bytes, stream);
+}
+
+moe_status moe_route_scores(const moe_config* cfg, const void* x, const void* Wg, const float* bg,
+                            int32_t* topk_idx, float* topk_w, float* gap, float* prob_mean, float* z_loss,
+                            float* scores, void* ws, size_t ws_bytes, moe_stream_t stream) {
   moe_status st = check_config(cfg);
   if (st != MOE_OK) return st;
   const moe_config& c = *cfg;
   if (c.T > 0 && (x == nullptr || Wg == nullptr || topk_idx == nullptr || topk_w == nullptr || gap == nullptr))
     return MOE_ERR_ARG;
   if (!aligned16(x) || !aligned16(Wg) || !aligned4(bg) || !aligned4(topk_idx) || !aligned4(topk_w) ||
-      !aligned4(gap) || !aligned4(prob_mean) || !aligned4(z_loss))
+      !aligned4(gap) || !aligned4(prob_mean) || !aligned4(z_loss) || !aligned4(scores))
     return MOE_ERR_ARG;
   const Scratch sc = scratch_layout(c);
   if ((st = check_ws(ws, ws_bytes, sc.total)) != MOE_OK) return st;
@@ -396,7 +402,7 @@ moe_status moe_route(const moe_config* cfg, const void* x, const void* Wg, const
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_route(c, x, Wg, bg, topk_idx, topk_w, gap, at<int32_t>(ws, sc.hist),
                                at<float>(ws, sc.psum), at<int32_t>(ws, sc.ntie), at<float>(ws, sc.zsum),
-                               at<uint32_t>(ws, sc.status), s);
+                               at<uint32_t>(ws, sc.status), s, scores);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   if (c.T == 0) {   // empty batch: P_e and the z-loss are not defined
     if (prob_mean != nullptr && cudaMemsetAsync(prob_mean, 0xff, sizeof(float) * (size_t)c.E, s) != cudaSuccess)
@@ -493,6 +499,12 @@ moe_status moe_combine(const moe_config* cfg, const void* yp, const int32_t* row
 moe_status moe_layer_forward(const moe_config* cfg, const void* x, const void* Wg, const float* bg,
                              const void* W1, const void* W2, void* out, moe_stats* stats,
                              void* ws, size_t ws_bytes, moe_stream_t stream) {
+  return moe_layer_forward_scores(cfg, x, Wg, bg, W1, W2, out, stats, nullptr, ws, ws_bytes, stream);
+}
+
+moe_status moe_layer_forward_scores(const moe_config* cfg, const void* x, const void* Wg, const float* bg,
+                                    const void* W1, const void* W2, void* out, moe_stats* stats, float* scores,
+                                    void* ws, size_t ws_bytes, moe_stream_t stream) {
   moe_status st = check_config(cfg);
   if (st != MOE_OK) return st;
   const moe_config& c = *cfg;
@@ -500,7 +512,7 @@ moe_status moe_layer_forward(const moe_config* cfg, const void* x, const void* W
   if (c.T > 0 && (x == nullptr || Wg == nullptr || W1 == nullptr || W2 == nullptr || out == nullptr))
     return MOE_ERR_ARG;
   if (!aligned16(x) || !aligned16(Wg) || !aligned4(bg) || !aligned16(W1) || !aligned16(W2) ||
-      !aligned16(out) || !aligned4(stats))
+      !aligned16(out) || !aligned4(stats) || !aligned4(scores))
     return MOE_ERR_ARG;
   const moe_ws_layout L = layout_of(c);
   if ((st = check_ws(ws, ws_bytes, L.total)) != MOE_OK) return st;
@@ -533,7 +545,7 @@ moe_status moe_layer_forward(const moe_config* cfg, const void* x, const void* W
   // histograms (the scatter scans them itself)
   cudaError_t e = launch_route(c, x, Wg, bg, idx, w, at<float>(ws, L.gap), at<int32_t>(scr, sc.hist),
                                at<float>(scr, sc.psum), at<int32_t>(scr, sc.ntie), at<float>(scr, sc.zsum),
-                               &stats->status, s);
+                               &stats->status, s, scores);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   float* row_w = at<float>(ws, L.row_w);
   float* out_f = static_cast<float*>(out);
@@ -735,6 +747,15 @@ moe_status moe_layer_backward(const moe_config* cfg, const void* x, const void* 
                               const void* W2, const float* dout, float aux_coef, float z_coef, const void* fws,
                               size_t fws_bytes, float* dx, float* dWg, float* dbg, float* dW1, float* dW2,
                               float* dw, moe_stats* stats, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  return moe_layer_backward_scores(cfg, x, Wg, bg, W1, W2, dout, nullptr, aux_coef, z_coef, fws, fws_bytes, dx, dWg, dbg,
+                                   dW1, dW2, dw, stats, ws, ws_bytes, stream);
+}
+
+moe_status moe_layer_backward_scores(const moe_config* cfg, const void* x, const void* Wg, const float* bg,
+                                     const void* W1, const void* W2, const float* dout, const float* dscores,
+                                     float aux_coef, float z_coef, const void* fws, size_t fws_bytes, float* dx,
+                                     float* dWg, float* dbg, float* dW1, float* dW2, float* dw, moe_stats* stats,
+                                     void* ws, size_t ws_bytes, moe_stream_t stream) {
   moe_status st = check_config(cfg);
   if (st != MOE_OK) return st;
   const moe_config& c = *cfg;
@@ -744,7 +765,7 @@ moe_status moe_layer_backward(const moe_config* cfg, const void* x, const void* 
   if (c.T > 0 && (x == nullptr || dout == nullptr || dx == nullptr)) return MOE_ERR_ARG;
   if (!aligned16(x) || !aligned16(Wg) || !aligned4(bg) || !aligned16(W1) || !aligned16(W2) || !aligned16(dout) ||
       !aligned16(dx) || !aligned16(dWg) || !aligned4(dbg) || !aligned16(dW1) || !aligned16(dW2) || !aligned4(dw) ||
-      !aligned4(stats))
+      !aligned4(dscores) || !aligned4(stats))
     return MOE_ERR_ARG;
   if (!isfinite(aux_coef) || !isfinite(z_coef)) return MOE_ERR_ARG;
   const moe_ws_layout FL = layout_of(c);
@@ -812,7 +833,7 @@ moe_status moe_layer_backward(const moe_config* cfg, const void* x, const void* 
   }
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   // the gate: scores, logits, dx and dW_gate
-  return cuda_status(launch_bwd_gate(c, x, Wg, bg, b, aux_coef, z_coef, dx, dWg, dbg, dw, s));
+  return cuda_status(launch_bwd_gate(c, x, Wg, bg, b, aux_coef, z_coef, dx, dWg, dbg, dw, s, dscores));
 }
 
 size_t moe_mxfp8_weight_bytes(const moe_config* cfg, size_t* w1q, size_t* w1s, size_t* w2q, size_t* w2s) {

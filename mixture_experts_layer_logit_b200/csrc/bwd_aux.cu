@@ -258,7 +258,7 @@ logits_kernel(const TX* __restrict__ x, const TX* __restrict__ wg, int T, int d,
 //            (0 for a dropped slot);
 //   dp     = (dw_i - sum_j w_j dw_j) / sum(p_sel) on the selected experts,
 //            plus aux_coef * E * f_e / T everywhere (f_e = counts_e / (T k));
-//   ds     = p (dp - <dp, p>) + z_coef * (2 / T) * lse * p;
+//   ds     = p (dp - <dp, p>) + z_coef * (2 / T) * lse * p (+ dscores);
 //   dz     = ds, or through z_hat = lambda (z - mean) / std:
 //            (lambda / std) (ds - mean(ds) - n mean(ds n)), 0 at zero spread.
 // The softmax is recomputed from the fp32 logits the way the route kernel
@@ -269,7 +269,8 @@ gate_bwd_kernel(const float* __restrict__ zpart, int nks, const float* __restric
                 const int32_t* __restrict__ row_of, const int32_t* __restrict__ offsets,
                 const int32_t* __restrict__ pad_offsets, const int32_t* __restrict__ counts,
                 const float* __restrict__ dwpart, int nt2, int rows_alloc, int T, int E, int k, float lam,
-                float aux_coef, float z_coef, float* __restrict__ dz, float* __restrict__ dw_out) {
+                float aux_coef, float z_coef, const float* __restrict__ dscores, float* __restrict__ dz,
+                float* __restrict__ dw_out) {
   constexpr int PER = kMaxExperts / 32;
   pdl_wait();
   pdl_launch_dependents();
@@ -368,6 +369,11 @@ gate_bwd_kernel(const float* __restrict__ zpart, int nks, const float* __restric
   const float zs = z_coef * 2.f / (float)T * lse;
 #pragma unroll
   for (int i = 0; i < PER; ++i) ds[i] = ok[i] ? p[i] * (dp[i] - dpp) + zs * p[i] : 0.f;
+  if (dscores != nullptr) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (ok[i]) ds[i] += dscores[(size_t)t * E + lane + 32 * i];
+  }
   if (lam > 0.f) {
     if (sd != 0.f) {
       float a = 0.f, b = 0.f;
@@ -560,7 +566,7 @@ cudaError_t launch_bwd_front_t(const moe_config& c, const void* x, const float* 
 template <typename TX>
 cudaError_t launch_bwd_gate_t(const moe_config& c, const void* x, const void* wg, const float* bg,
                               const BwdState& st, float aux_coef, float z_coef, float* dx, float* dwg, float* dbg,
-                              float* dw_out, cudaStream_t s) {
+                              float* dw_out, const float* dscores, cudaStream_t s) {
   const TX* X = static_cast<const TX*>(x);
   const TX* WG = static_cast<const TX*>(wg);
   const int nks = bwd_logit_slices(c);
@@ -573,8 +579,8 @@ cudaError_t launch_bwd_gate_t(const moe_config& c, const void* x, const void* wg
   const int nt2 = (c.F + col - 1) / col;
   e = launch_pdl(gate_bwd_kernel, dim3((c.T + 7) / 8), dim3(256), 0, s, (const float*)st.z, nks, bg, st.topk_idx,
                  st.topk_w, st.row_of, st.offsets, (const int32_t*)st.pad_offsets, st.counts,
-                 (const float*)st.dwpart, nt2, st.rows_alloc, c.T, c.E, c.k, c.lambda, aux_coef, z_coef, st.dz,
-                 dw_out);
+                 (const float*)st.dwpart, nt2, st.rows_alloc, c.T, c.E, c.k, c.lambda, aux_coef, z_coef, dscores,
+                 st.dz, dw_out);
   if (e != cudaSuccess) return e;
   e = launch_pdl(dx_kernel<TX>, dim3((c.T + 15) / 16, (c.d + 511) / 512), dim3(128), 0, s, (const float*)st.dxp,
                  (const float*)st.dz, WG, st.topk_idx, st.row_of, st.offsets, (const int32_t*)st.pad_offsets, c.T,
@@ -610,10 +616,10 @@ cudaError_t launch_bwd_front(const moe_config& c, const void* x, const float* do
 
 cudaError_t launch_bwd_gate(const moe_config& c, const void* x, const void* wg, const float* bg, const BwdState& st,
                             float aux_coef, float z_coef, float* dx, float* dwg, float* dbg, float* dw_out,
-                            cudaStream_t s) {
+                            cudaStream_t s, const float* dscores) {
   if (c.dtype == MOE_DTYPE_BF16)
-    return launch_bwd_gate_t<__nv_bfloat16>(c, x, wg, bg, st, aux_coef, z_coef, dx, dwg, dbg, dw_out, s);
-  return launch_bwd_gate_t<float>(c, x, wg, bg, st, aux_coef, z_coef, dx, dwg, dbg, dw_out, s);
+    return launch_bwd_gate_t<__nv_bfloat16>(c, x, wg, bg, st, aux_coef, z_coef, dx, dwg, dbg, dw_out, dscores, s);
+  return launch_bwd_gate_t<float>(c, x, wg, bg, st, aux_coef, z_coef, dx, dwg, dbg, dw_out, dscores, s);
 }
 
 }  // namespace moe

@@ -39,15 +39,16 @@ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Route: logits, normalisation, softmax, top-k; per-chunk histogram, probability
 // sums, near-tie counts and z-loss sums into scratch.  TX = float or __nv_bfloat16.
+// scores[T][E] fp32, when given, receives the scores that the softmax takes.
 cudaError_t launch_route(const moe_config& c, const void* x, const void* wg, const float* bg,
                          int32_t* topk_idx, float* topk_w, float* gap,
                          int32_t* hist, float* psum, int32_t* ntie, float* zsum, uint32_t* status,
-                         cudaStream_t s);
+                         cudaStream_t s, float* scores = nullptr);
 // The same on tcgen05 tensor cores (bf16, k <= 8).
 bool route_tc_supported(const moe_config& c);
 cudaError_t launch_route_tc(const moe_config& c, const void* x, const void* wg, const float* bg,
                             int32_t* topk_idx, float* topk_w, float* gap, int32_t* hist, float* psum,
-                            int32_t* ntie, float* zsum, uint32_t* status, cudaStream_t s);
+                            int32_t* ntie, float* zsum, uint32_t* status, cudaStream_t s, float* scores = nullptr);
 // One launch: prob_mean[e] = sum over chunks of psum / T and *z_loss = sum over
 // chunks of zsum / T, both in a fixed order; either output may be NULL.
 cudaError_t launch_route_totals(const moe_config& c, const float* psum, const float* zsum, float* prob_mean,
@@ -173,10 +174,11 @@ cudaError_t launch_grouped_plain_tc_pair(const moe_config& c, const void* A, con
                                          cudaStream_t s);
 cudaError_t launch_grouped_plain_simt(const moe_config& c, const void* A, const int32_t* offsets, int rows_alloc,
                                       const void* B, int K, int Nout, float* out, uint32_t* status, cudaStream_t s);
-// the gate's gradient (logits recomputed), dx and dW_gate / db
+// the gate's gradient (logits recomputed), dx and dW_gate / db; dscores[T][E],
+// when given, is added to the gradient of the scores
 cudaError_t launch_bwd_gate(const moe_config& c, const void* x, const void* wg, const float* bg, const BwdState& st,
                             float aux_coef, float z_coef, float* dx, float* dwg, float* dbg, float* dw_out,
-                            cudaStream_t s);
+                            cudaStream_t s, const float* dscores = nullptr);
 
 // ------------------------------------------------------- MX FP8 experts
 // Buffers of the FP8 expert step: kept offsets from the permutation, padded

@@ -67,7 +67,7 @@ route_kernel(const TX* __restrict__ x, const TX* __restrict__ wg, const float* _
              int T, int d, int E, int k, float lam,
              int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, float* __restrict__ gap_out,
              int32_t* __restrict__ hist_out, float* __restrict__ psum_out, int32_t* __restrict__ ntie_out,
-             float* __restrict__ zsum_out, int nch, uint32_t* __restrict__ status) {
+             float* __restrict__ zsum_out, int nch, uint32_t* __restrict__ status, float* __restrict__ scores) {
   using L = RouteSmem<NJ>;
   constexpr int EP = L::EP;
   constexpr int V = VecLoad<TX>::N;
@@ -182,6 +182,11 @@ route_kernel(const TX* __restrict__ x, const TX* __restrict__ wg, const float* _
       const float sd = sqrtf(warp_sum(q) / (float)E);
 #pragma unroll
       for (int i = 0; i < EPL; ++i) v[i] = (sd == 0.f) ? 0.f : lam * (v[i] - mu) / sd;   // NaN spread stays NaN
+    }
+    if (scores != nullptr) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (ok[i]) scores[(size_t)t * E + lane + 32 * i] = v[i];
     }
     float m = -INFINITY;
 #pragma unroll
@@ -312,7 +317,7 @@ __global__ void route_totals_kernel(const float* __restrict__ psum, const float*
 template <int NJ, typename TX>
 cudaError_t launch_route_nj(const moe_config& c, const void* x, const void* wg, const float* bg,
                             int32_t* idx, float* w, float* gap, int32_t* hist, float* psum,
-                            int32_t* ntie, float* zsum, uint32_t* status, cudaStream_t s) {
+                            int32_t* ntie, float* zsum, uint32_t* status, float* scores, cudaStream_t s) {
   const size_t smem = RouteSmem<NJ>::total;
   auto kern = route_kernel<NJ, TX>;
   cudaError_t err = set_smem_once<route_kernel<NJ, TX>>(smem);
@@ -320,19 +325,19 @@ cudaError_t launch_route_nj(const moe_config& c, const void* x, const void* wg, 
   const int nch = num_chunks(c.T);
   kern<<<nch, kThreads, smem, s>>>(static_cast<const TX*>(x), static_cast<const TX*>(wg), bg,
                                    c.T, c.d, c.E, c.k, c.lambda, idx, w, gap, hist, psum, ntie, zsum, nch,
-                                   status);
+                                   status, scores);
   return cudaGetLastError();
 }
 
 template <typename TX>
 cudaError_t launch_route_t(const moe_config& c, const void* x, const void* wg, const float* bg,
                            int32_t* idx, float* w, float* gap, int32_t* hist, float* psum,
-                           int32_t* ntie, float* zsum, uint32_t* status, cudaStream_t s) {
-  if (c.E <= 16) return launch_route_nj<1, TX>(c, x, wg, bg, idx, w, gap, hist, psum, ntie, zsum, status, s);
-  if (c.E <= 32) return launch_route_nj<2, TX>(c, x, wg, bg, idx, w, gap, hist, psum, ntie, zsum, status, s);
-  if (c.E <= 64) return launch_route_nj<4, TX>(c, x, wg, bg, idx, w, gap, hist, psum, ntie, zsum, status, s);
-  if (c.E <= 128) return launch_route_nj<8, TX>(c, x, wg, bg, idx, w, gap, hist, psum, ntie, zsum, status, s);
-  return launch_route_nj<16, TX>(c, x, wg, bg, idx, w, gap, hist, psum, ntie, zsum, status, s);
+                           int32_t* ntie, float* zsum, uint32_t* status, float* scores, cudaStream_t s) {
+  if (c.E <= 16) return launch_route_nj<1, TX>(c, x, wg, bg, idx, w, gap, hist, psum, ntie, zsum, status, scores, s);
+  if (c.E <= 32) return launch_route_nj<2, TX>(c, x, wg, bg, idx, w, gap, hist, psum, ntie, zsum, status, scores, s);
+  if (c.E <= 64) return launch_route_nj<4, TX>(c, x, wg, bg, idx, w, gap, hist, psum, ntie, zsum, status, scores, s);
+  if (c.E <= 128) return launch_route_nj<8, TX>(c, x, wg, bg, idx, w, gap, hist, psum, ntie, zsum, status, scores, s);
+  return launch_route_nj<16, TX>(c, x, wg, bg, idx, w, gap, hist, psum, ntie, zsum, status, scores, s);
 }
 
 }  // namespace
@@ -340,13 +345,14 @@ cudaError_t launch_route_t(const moe_config& c, const void* x, const void* wg, c
 cudaError_t launch_route(const moe_config& c, const void* x, const void* wg, const float* bg,
                          int32_t* topk_idx, float* topk_w, float* gap,
                          int32_t* hist, float* psum, int32_t* ntie, float* zsum, uint32_t* status,
-                         cudaStream_t s) {
+                         cudaStream_t s, float* scores) {
   if (c.T == 0) return cudaSuccess;
   if (route_tc_supported(c))
-    return launch_route_tc(c, x, wg, bg, topk_idx, topk_w, gap, hist, psum, ntie, zsum, status, s);
+    return launch_route_tc(c, x, wg, bg, topk_idx, topk_w, gap, hist, psum, ntie, zsum, status, s, scores);
   if (c.dtype == MOE_DTYPE_BF16)
-    return launch_route_t<__nv_bfloat16>(c, x, wg, bg, topk_idx, topk_w, gap, hist, psum, ntie, zsum, status, s);
-  return launch_route_t<float>(c, x, wg, bg, topk_idx, topk_w, gap, hist, psum, ntie, zsum, status, s);
+    return launch_route_t<__nv_bfloat16>(c, x, wg, bg, topk_idx, topk_w, gap, hist, psum, ntie, zsum, status, scores,
+                                         s);
+  return launch_route_t<float>(c, x, wg, bg, topk_idx, topk_w, gap, hist, psum, ntie, zsum, status, scores, s);
 }
 
 cudaError_t launch_route_totals(const moe_config& c, const float* psum, const float* zsum, float* prob_mean,

@@ -169,12 +169,13 @@ static_assert(sizeof(RSlots) <= sizeof(RLists), "the slots reuse the lists' spac
 // sorted local lists, ordered by score and then by the lower index, so the
 // lowest index wins equal scores, and the first round's winner is the row's
 // maximum.  Afterwards Z holds the row's softmax probabilities (zeros for an
-// invalid row); lane j < k writes slot j.
+// invalid row); lane j < k writes slot j.  scores, when given, receives the
+// row's scores (z, or z_hat).
 template <int KB>
 __device__ __forceinline__ void gate_row_warp(float* Z, int E, float lam, int t, bool valid, int lane,
                                               int32_t* __restrict__ topk_idx, float* __restrict__ topk_w,
                                               float* __restrict__ gap_out, int* hist, int* ntie, float* zrow,
-                                              uint32_t* status) {
+                                              uint32_t* status, float* __restrict__ scores) {
   constexpr int k = KB;
   if (lam > 0.f) {   // z_hat = lambda (z - mean) / std, written over z
     float s = 0.f;
@@ -188,6 +189,8 @@ __device__ __forceinline__ void gate_row_warp(float* Z, int E, float lam, int t,
     const float sd = sqrtf(warp_sum(qq) / (float)E);
     for (int e = lane; e < E; e += 32) Z[e] = gate_score(Z[e], lam, mu, sd);
   }
+  if (scores != nullptr && valid)
+    for (int e = lane; e < E; e += 32) scores[(size_t)t * E + e] = Z[e];
   TopList<KB> top;
   top.init();
   for (int e = lane; e < E; e += 32) top.template insert<KB + 1>(Z[e], e);
@@ -270,7 +273,8 @@ route_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                 const float* __restrict__ bg, int T, int d, int E, int EP, int nst, float lam,
                 int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, float* __restrict__ gap_out,
                 int32_t* __restrict__ hist_out, float* __restrict__ psum_out, int32_t* __restrict__ ntie_out,
-                float* __restrict__ zsum_out, int nch, uint32_t* __restrict__ status, int lists_off, int nks) {
+                float* __restrict__ zsum_out, int nch, uint32_t* __restrict__ status, int lists_off, int nks,
+                float* __restrict__ scores_out) {
   constexpr int k = KB;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -432,7 +436,7 @@ route_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     __syncthreads();
     for (int r = r0 + warp; r < r1; r += kThreads / 32)
       gate_row_warp<KB>(Zall + (size_t)r * ldz, E, lam, t0 + r, ok, lane, topk_idx, topk_w, gap_out, tail->hist,
-                        &tail->ntie, &tail->zrow[r], status);
+                        &tail->ntie, &tail->zrow[r], status, scores_out);
     __syncthreads();
     // this CTA's probability sums over its rows: nG groups of rows, the group
     // partials added in group order
@@ -524,6 +528,14 @@ route_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       }
     }
     __syncthreads();
+    if (scores_out != nullptr) {   // the chunk's scores, whole rows of them, before the exponentials replace them
+      const int nel = ok ? min(RM, T - t0) * E : 0;
+      for (int i = tid; i < nel; i += kThreads) {
+        const int r = i / E, e = i - r * E;
+        scores_out[(size_t)t0 * E + i] = Zall[(size_t)r * ldz + e];
+      }
+      __syncthreads();
+    }
     const float m = fmaxf(fmaxf(part[0][2][row], part[1][2][row]), fmaxf(part[2][2][row], part[3][2][row]));
     float Sh = 0.f;
 #pragma unroll 4
@@ -625,7 +637,7 @@ int kslices(const moe_config& c, long long sms) {
 template <int KB, bool SPLIT>
 cudaError_t launch_ks(const moe_config& c, const CUtensorMap& mx, const CUtensorMap& mw, int EP, const float* bg,
                       int32_t* idx, float* w, float* gap, int32_t* hist, float* psum, int32_t* ntie,
-                      float* zsum, uint32_t* status, int nks, cudaStream_t s) {
+                      float* zsum, uint32_t* status, int nks, float* scores, cudaStream_t s) {
   // the most any E <= kMaxExperts needs, so one attribute serves every launch
   static const size_t kMaxSmem = [] {
     size_t m = 0;
@@ -652,19 +664,19 @@ cudaError_t launch_ks(const moe_config& c, const CUtensorMap& mx, const CUtensor
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, route_tc_kernel<KB, SPLIT>, mx, mw, bg, c.T, c.d, c.E, EP, num_stages(EP),
                             c.lambda, idx, w, gap, hist, psum, ntie, zsum, nch, status, (int)lists_offset(c.E, EP),
-                            nks);
+                            nks, scores);
 }
 
 template <int KB>
 cudaError_t launch_kb(const moe_config& c, const CUtensorMap& mx, const CUtensorMap& mw, int EP, const float* bg,
                       int32_t* idx, float* w, float* gap, int32_t* hist, float* psum, int32_t* ntie,
-                      float* zsum, uint32_t* status, cudaStream_t s) {
+                      float* zsum, uint32_t* status, float* scores, cudaStream_t s) {
   DeviceInfo di;
   cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
   const int nks = kslices(c, di.sms);
-  return nks > 1 ? launch_ks<KB, true>(c, mx, mw, EP, bg, idx, w, gap, hist, psum, ntie, zsum, status, nks, s)
-                 : launch_ks<KB, false>(c, mx, mw, EP, bg, idx, w, gap, hist, psum, ntie, zsum, status, 1, s);
+  return nks > 1 ? launch_ks<KB, true>(c, mx, mw, EP, bg, idx, w, gap, hist, psum, ntie, zsum, status, nks, scores, s)
+                 : launch_ks<KB, false>(c, mx, mw, EP, bg, idx, w, gap, hist, psum, ntie, zsum, status, 1, scores, s);
 }
 
 }  // namespace
@@ -673,7 +685,7 @@ bool route_tc_supported(const moe_config& c) { return c.dtype == MOE_DTYPE_BF16 
 
 cudaError_t launch_route_tc(const moe_config& c, const void* x, const void* wg, const float* bg,
                             int32_t* topk_idx, float* topk_w, float* gap, int32_t* hist, float* psum,
-                            int32_t* ntie, float* zsum, uint32_t* status, cudaStream_t s) {
+                            int32_t* ntie, float* zsum, uint32_t* status, cudaStream_t s, float* scores) {
   if (c.T == 0) return cudaSuccess;
   const int EP = ((c.E + 15) / 16) * 16;
   CUtensorMap mx, mw;
@@ -681,7 +693,7 @@ cudaError_t launch_route_tc(const moe_config& c, const void* x, const void* wg, 
       !make_map(&mw, wg, (uint64_t)c.E, (uint64_t)c.d, false, (uint32_t)EP))
     return cudaErrorInvalidValue;
 #define MOE_ROUTE_K(K) \
-  case K: return launch_kb<K>(c, mx, mw, EP, bg, topk_idx, topk_w, gap, hist, psum, ntie, zsum, status, s)
+  case K: return launch_kb<K>(c, mx, mw, EP, bg, topk_idx, topk_w, gap, hist, psum, ntie, zsum, status, scores, s)
   switch (c.k) {
     MOE_ROUTE_K(1); MOE_ROUTE_K(2); MOE_ROUTE_K(3); MOE_ROUTE_K(4);
     MOE_ROUTE_K(5); MOE_ROUTE_K(6); MOE_ROUTE_K(7); MOE_ROUTE_K(8);
