@@ -533,7 +533,7 @@ moe_status moe_balance_loss(const moe_balance_config* cfg, const void* scores, c
  *     least the smallest code; a value that is not finite gets the NaN code.
  *     The update itself uses the unrounded m and v.  A new state is zeros
  *     throughout, for 32 and for 8 bits.
- *   hyper (host): finite lr, 0 <= beta1, beta2 < 1, eps > 0.
+ *   hyper (host): finite lr, 0 <= beta1, beta2 < 1, eps > 0 (a normal fp32 number).
  *   lr: device fp32 scalar, used instead of hyper->lr, or NULL.
  *   grad_scale: device fp32 scalar or NULL (1): gradient clipping, loss scaling.
  *   state (device): step is advanced by one by the call, ticket is zero between

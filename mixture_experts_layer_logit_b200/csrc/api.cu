@@ -695,7 +695,7 @@ moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t ntensors, con
   if (ntensors < 0 || (ntensors > 0 && tensors == nullptr) || hyper == nullptr || state == nullptr)
     return MOE_ERR_ARG;
   if (!isfinite(hyper->lr) || !(hyper->beta1 >= 0.0 && hyper->beta1 < 1.0) ||
-      !(hyper->beta2 >= 0.0 && hyper->beta2 < 1.0) || !isfinite(hyper->eps) || !((float)hyper->eps > 0.f))
+      !(hyper->beta2 >= 0.0 && hyper->beta2 < 1.0) || !((float)hyper->eps >= 0x1p-126f) || !isfinite((float)hyper->eps))
     return MOE_ERR_ARG;
   if (!aligned4(lr) || !aligned4(grad_scale) || !aligned4(state)) return MOE_ERR_ARG;
   moe_status st;
