@@ -90,44 +90,32 @@ __device__ __forceinline__ float reciprocal(float v) {
   return r;
 }
 
-// max |v| over the warp's block as float bits
-__device__ __forceinline__ unsigned block_top(const float (&v)[8]) {
-  unsigned top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-  return __reduce_max_sync(0xffffffffu, top);
+// sqrt(v) rounded to nearest for 2^-100 <= v < inf, without the library's
+// branch for the other values: with y near 1 / sqrt(v) and s = v y, the residual
+// v - s s is exact in one FMA and s + (v - s s) y / 2 rounds correctly
+// (Markstein's correction step; compared with sqrtf for every float of that range).
+constexpr float kRootLow = 0x1p-100f;
+__device__ __forceinline__ float root_in_range(float v) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
+  const float s = __fmul_rn(v, y);
+  return __fmaf_rn(__fmaf_rn(-s, s, v), __fmul_rn(y, 0.5f), s);
 }
 
-// Codes of the warp's block of eight values a lane, element i in byte i, and
-// (returned) the scale.  The fast path takes a block of finite values, roots
-// none of which is zero: they are lifted to the smallest code by a maximum.
+// Codes of the warp's block of eight values a lane, element i in byte i.  inv
+// brings the block's largest finite |v| to 448.  ODD: some value is not finite
+// or some root is zero.  Otherwise roots are lifted to the smallest code by a
+// maximum, and the conversion's NaN code is the one wanted.
 template <bool ROOT>
-__device__ __forceinline__ float encode(const float (&v)[8], uint2* codes) {
-  unsigned top = block_top(v);
-  bool odd = top >= 0x7f800000u;
-  if (odd) {   // an inf or NaN: the largest of the others
-    top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (isfinite(v[i])) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-    top = __reduce_max_sync(0xffffffffu, top);
-  }
-  const float most = fmaxf(__uint_as_float(top), 0x1p-100f);   // its reciprocal stays finite
-  const float2 inv = both(__fmul_rn(__frcp_rn(most), 448.f));
-  if (ROOT) {
-    float least = v[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) least = fminf(least, v[i]);
-    odd |= __any_sync(0xffffffffu, least == 0.f);
-  }
+__device__ __forceinline__ uint2 encode(const float (&v)[8], float inv, bool odd) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float2 q = mul2(make_float2(v[2 * i], v[2 * i + 1]), inv);
+    float2 q = mul2(make_float2(v[2 * i], v[2 * i + 1]), both(inv));
     if (ROOT) q = make_float2(fmaxf(q.x, 0x1p-9f), fmaxf(q.y, 0x1p-9f));
     w[i] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
   }
-  if (odd) {   // zeros and NaNs put right
+  if (odd) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (ROOT && v[2 * i] == 0.f) w[i] &= 0xff00u;
@@ -136,8 +124,16 @@ __device__ __forceinline__ float encode(const float (&v)[8], uint2* codes) {
       if (!isfinite(v[2 * i + 1])) w[i] = (w[i] & 0xffu) | 0x7f00u;
     }
   }
-  *codes = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-  return __fmul_rn(most, 1.f / 448.f);
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// The largest finite |v| of the warp's block
+__device__ __forceinline__ float finite_top(const float (&v)[8]) {
+  unsigned top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (isfinite(v[i])) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
 }
 
 __device__ __forceinline__ void decode(uint2 c, float scale, float (&v)[8]) {
@@ -162,84 +158,155 @@ __device__ __forceinline__ void store_codes1(unsigned char* p, int count, int la
     if (i * 32 + lane < count) p[i * 32 + lane] = (unsigned char)((i < 4 ? c.x : c.y) >> (8 * (i % 4)));
 }
 
-// One warp, one block of 256 elements from b0 on.  VEC: all there, every array
-// aligned to eight of its elements, lane l holds elements 8 l .. 8 l + 7; else
-// elements l, l + 32, ... below `count`, one by one.  Every load is issued
-// before the first value is used.
+// A lane's share of a block of 256 elements as it was loaded.
+template <int BITS>
+struct Raw {
+  Raw8 g, p, m, v;
+};
+template <>
+struct Raw<8> {
+  Raw8 g, p;
+  uint2 m, v;
+  float ms, vs;
+};
+
+// One warp, one block of 256 elements from b0 on.  Lane l holds elements l,
+// l + 32, ... as far as the tensor goes, loaded one by one.
+template <int BITS>
+__device__ __forceinline__ void load_single(Raw<BITS>& r, const Entry& e, long long b0, int lane) {
+  const void* psrc = e.master != nullptr ? e.master : e.param;
+  const int psdt = e.master != nullptr ? MOE_DTYPE_F32 : e.pdt;
+  const int count = (int)min((long long)kBlock, e.n - b0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const long long at = b0 + i * 32 + lane;
+    const bool here = i * 32 + lane < count;
+    r.g.w[i] = here ? load_raw1(e.grad, e.gdt, at) : 0u;
+    r.p.w[i] = here ? load_raw1(psrc, psdt, at) : 0u;
+    if constexpr (BITS == 32) {
+      r.m.w[i] = here ? load_raw1(e.m, MOE_DTYPE_F32, at) : 0u;
+      r.v.w[i] = here ? load_raw1(e.v, MOE_DTYPE_F32, at) : 0u;
+    }
+  }
+  if constexpr (BITS == 8) {
+    r.ms = e.ms[b0 / kBlock];
+    r.vs = e.vs[b0 / kBlock];
+    r.m = load_codes1(static_cast<const unsigned char*>(e.m) + b0, count, lane);
+    r.v = load_codes1(static_cast<const unsigned char*>(e.v) + b0, count, lane);
+  }
+}
+
+// A whole block through shared memory: the warp copies the next blocks' bytes
+// in whole lines while it works on one, and a lane reads its eight consecutive
+// elements from there.
+template <int BITS>
+struct Stage {
+  static constexpr int g = 0, p = 1024, m = 2048, v = BITS == 8 ? 2304 : 3072, bytes = BITS == 8 ? 2560 : 4096;
+  static constexpr int count = 2;
+};
+constexpr int kWarpStage = Stage<8>::bytes * Stage<8>::count > Stage<32>::bytes * Stage<32>::count
+                               ? Stage<8>::bytes * Stage<8>::count
+                               : Stage<32>::bytes * Stage<32>::count;
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+// 256 elements of type dt, 1024 or 512 bytes
+__device__ __forceinline__ void copy_row(uint32_t to, const void* p, int dt, long long i, int lane) {
+  const char* from = static_cast<const char*>(p) + i * (dt == MOE_DTYPE_F32 ? 4 : 2) + lane * 16;
+  copy16(to + lane * 16, from);
+  if (dt == MOE_DTYPE_F32) copy16(to + 512 + lane * 16, from + 512);
+}
+template <int BITS>
+__device__ __forceinline__ void copy_block(uint32_t st, const Entry& e, long long b0, int lane) {
+  copy_row(st + Stage<BITS>::g, e.grad, e.gdt, b0, lane);
+  if (e.master != nullptr) copy_row(st + Stage<BITS>::p, e.master, MOE_DTYPE_F32, b0, lane);
+  else copy_row(st + Stage<BITS>::p, e.param, e.pdt, b0, lane);
+  if constexpr (BITS == 8) {   // 16 lanes each for the codes of m and v, which lie one after the other
+    const char* from = static_cast<const char*>(lane < 16 ? e.m : e.v) + b0 + (lane & 15) * 16;
+    copy16(st + Stage<8>::m + lane * 16, from);
+  } else {
+    copy_row(st + Stage<32>::m, e.m, MOE_DTYPE_F32, b0, lane);
+    copy_row(st + Stage<32>::v, e.v, MOE_DTYPE_F32, b0, lane);
+  }
+}
+
+__device__ __forceinline__ void shared8(Raw8& r, uint32_t at, int dt, int lane) {
+  at += lane * (dt == MOE_DTYPE_F32 ? 32 : 16);
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "r"(at));
+  if (dt == MOE_DTYPE_F32)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7]) : "r"(at + 16));
+}
+template <int BITS>
+__device__ __forceinline__ void load_staged(Raw<BITS>& r, uint32_t st, const Entry& e, int lane) {
+  shared8(r.g, st + Stage<BITS>::g, e.gdt, lane);
+  shared8(r.p, st + Stage<BITS>::p, e.master != nullptr ? MOE_DTYPE_F32 : e.pdt, lane);
+  if constexpr (BITS == 8) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.m.x), "=r"(r.m.y) : "r"(st + Stage<8>::m + lane * 8));
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.v.x), "=r"(r.v.y) : "r"(st + Stage<8>::v + lane * 8));
+  } else {
+    shared8(r.m, st + Stage<32>::m, MOE_DTYPE_F32, lane);
+    shared8(r.v, st + Stage<32>::v, MOE_DTYPE_F32, lane);
+  }
+}
+
 template <bool VEC, int BITS>
-__device__ __forceinline__ void update_block(const Entry& e, long long b0, int lane, const Step& s) {
+__device__ __forceinline__ void update_block(const Raw<BITS>& r, const Entry& e, long long b0, int lane,
+                                             const Step& s) {
   const int count = VEC ? kBlock : (int)min((long long)kBlock, e.n - b0);
   const long long at = VEC ? b0 + lane * 8 : b0 + lane;
   const bool has_master = e.master != nullptr;
-  Raw8 rg, rp, rm, rv;
-  uint2 cm, cv;
-  float ms, vs;
-  if constexpr (BITS == 8) {
-    ms = e.ms[b0 / kBlock];
-    vs = e.vs[b0 / kBlock];
-  }
-  const void* psrc = has_master ? e.master : e.param;
   const int psdt = has_master ? MOE_DTYPE_F32 : e.pdt;
-  if constexpr (VEC) {
-    load8(rg, e.grad, e.gdt, at);
-    load8(rp, psrc, psdt, at);
-    if constexpr (BITS == 8) {
-      cm = __ldcs(reinterpret_cast<const uint2*>(static_cast<const unsigned char*>(e.m) + at));
-      cv = __ldcs(reinterpret_cast<const uint2*>(static_cast<const unsigned char*>(e.v) + at));
-    } else {
-      load8(rm, e.m, MOE_DTYPE_F32, at);
-      load8(rv, e.v, MOE_DTYPE_F32, at);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      rg.w[i] = rp.w[i] = rm.w[i] = rv.w[i] = 0u;
-      if (i * 32 + lane < count) {
-        rg.w[i] = load_raw1(e.grad, e.gdt, at + i * 32);
-        rp.w[i] = load_raw1(psrc, psdt, at + i * 32);
-        if constexpr (BITS == 32) {
-          rm.w[i] = load_raw1(e.m, MOE_DTYPE_F32, at + i * 32);
-          rv.w[i] = load_raw1(e.v, MOE_DTYPE_F32, at + i * 32);
-        }
-      }
-    }
-    if constexpr (BITS == 8) {
-      cm = load_codes1(static_cast<const unsigned char*>(e.m) + b0, count, lane);
-      cv = load_codes1(static_cast<const unsigned char*>(e.v) + b0, count, lane);
-    }
-  }
   float g[8], p[8], m[8], v[8], root[8];
   if constexpr (VEC) {
-    to_float8(rg, e.gdt, g);
-    to_float8(rp, psdt, p);
+    to_float8(r.g, e.gdt, g);
+    to_float8(r.p, psdt, p);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      g[i] = raw_to_float(rg.w[i], e.gdt);
-      p[i] = raw_to_float(rp.w[i], psdt);
+      g[i] = raw_to_float(r.g.w[i], e.gdt);
+      p[i] = raw_to_float(r.p.w[i], psdt);
     }
   }
   if constexpr (BITS == 8) {
-    decode(cm, ms, m);
-    decode(cv, vs, v);
+    decode(r.m, r.ms, m);
+    decode(r.v, r.vs, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], v[i]);
   } else {
-    to_float8(rm, MOE_DTYPE_F32, m);
-    to_float8(rv, MOE_DTYPE_F32, v);
+    to_float8(r.m, MOE_DTYPE_F32, m);
+    to_float8(r.v, MOE_DTYPE_F32, v);
   }
+  // the bits of v >= 0 order like v, an inf's and a NaN's above all others
+  unsigned low = ~0u, high = 0u;
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
     const float2 gi = mul2(make_float2(g[i], g[i + 1]), both(s.gs));
     const float2 mi = add2(mul2(make_float2(m[i], m[i + 1]), both(s.beta1)), mul2(gi, both(s.omb1)), both(s.one));
-    const float2 vi = add2(mul2(make_float2(v[i], v[i + 1]), both(s.beta2)), mul2(mul2(gi, gi), both(s.omb2)), both(s.one));
-    const float2 ri = make_float2(sqrtf(vi.x), sqrtf(vi.y));
-    const float2 den = fma2(ri, both(s.rc2), both(s.eps));
-    const float2 upd = mul2(mul2(mi, both(s.alpha)), make_float2(reciprocal(den.x), reciprocal(den.y)));
-    const float2 pi = fma2(make_float2(p[i], p[i + 1]), both(s.keep), upd);
+    const float2 vi =
+        add2(mul2(make_float2(v[i], v[i + 1]), both(s.beta2)), mul2(mul2(gi, gi), both(s.omb2)), both(s.one));
     m[i] = mi.x, m[i + 1] = mi.y;
     v[i] = vi.x, v[i + 1] = vi.y;
-    root[i] = ri.x, root[i + 1] = ri.y;
+    low = min(low, min(__float_as_uint(vi.x), __float_as_uint(vi.y)));
+    high = max(high, max(__float_as_uint(vi.x), __float_as_uint(vi.y)));
+  }
+  if constexpr (BITS == 8) high = __reduce_max_sync(0xffffffffu, high);   // for the scale
+  const bool odd = __any_sync(0xffffffffu, low < __float_as_uint(kRootLow) || high >= 0x7f800000u);
+  if (!odd) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) root[i] = root_in_range(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) root[i] = sqrtf(v[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 den = fma2(make_float2(root[i], root[i + 1]), both(s.rc2), both(s.eps));
+    const float2 upd = mul2(mul2(make_float2(m[i], m[i + 1]), both(s.alpha)),
+                            make_float2(reciprocal(den.x), reciprocal(den.y)));
+    const float2 pi = fma2(make_float2(p[i], p[i + 1]), both(s.keep), upd);
     p[i] = pi.x, p[i + 1] = pi.y;
   }
   if constexpr (VEC) {
@@ -262,10 +329,21 @@ __device__ __forceinline__ void update_block(const Entry& e, long long b0, int l
       }
   }
   if constexpr (BITS == 8) {   // elements past the end are zeros throughout: they do not raise the maximum
-    const float mscale = encode<false>(m, &cm), vscale = encode<true>(root, &cv);
+    float mt = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mt = fmaxf(mt, fabsf(m[i]));   // leaves NaN out
+    mt = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mt)));
+    const bool inf = mt == INFINITY;
+    if (inf) mt = finite_top(m);
+    // the largest root is the root of the largest v
+    float vt = odd ? finite_top(root) : root_in_range(__uint_as_float(high));
+    mt = fmaxf(mt, 0x1p-100f);   // the reciprocals stay finite
+    vt = fmaxf(vt, 0x1p-100f);
+    const uint2 cm = encode<false>(m, __fmul_rn(__frcp_rn(mt), 448.f), inf);
+    const uint2 cv = encode<true>(root, __fmul_rn(__frcp_rn(vt), 448.f), odd);
     if (lane == 0) {
-      e.ms[b0 / kBlock] = mscale;
-      e.vs[b0 / kBlock] = vscale;
+      e.ms[b0 / kBlock] = __fmul_rn(mt, 1.f / 448.f);
+      e.vs[b0 / kBlock] = __fmul_rn(vt, 1.f / 448.f);
     }
     unsigned char* pm = static_cast<unsigned char*>(e.m);
     unsigned char* pv = static_cast<unsigned char*>(e.v);
@@ -279,11 +357,56 @@ __device__ __forceinline__ void update_block(const Entry& e, long long b0, int l
   }
 }
 
+// The warp's blocks of one tensor's elements [b0, end), a tile apart.
+template <int BITS>
+__device__ __forceinline__ void run_tensor(const Entry& e, long long b0, long long end, uint32_t stages, int lane,
+                                           const Step& s) {
+  constexpr int N = Stage<BITS>::count;
+  if (e.vec) {
+    const int blocks = b0 + kBlock <= end ? (int)((end - kBlock - b0) / kTile) + 1 : 0;   // whole ones
+    float2 scale = make_float2(0.f, 0.f), ahead = scale;
+    auto scales = [&](int i) {
+      const long long k = (b0 + (long long)i * kTile) / kBlock;
+      return make_float2(e.ms[k], e.vs[k]);
+    };
+    if (BITS == 8 && blocks > 0) scale = scales(0);
+#pragma unroll
+    for (int i = 0; i < N - 1; ++i) {
+      if (i < blocks) copy_block<BITS>(stages + i * Stage<BITS>::bytes, e, b0 + (long long)i * kTile, lane);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    int at = 0, to = N - 1;
+    for (int i = 0; i < blocks; ++i) {
+      if (i + N - 1 < blocks)
+        copy_block<BITS>(stages + to * Stage<BITS>::bytes, e, b0 + (long long)(i + N - 1) * kTile, lane);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (BITS == 8 && i + 1 < blocks) ahead = scales(i + 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(N - 1) : "memory");
+      __syncwarp();   // every lane's part of the block has arrived
+      Raw<BITS> r;
+      load_staged<BITS>(r, stages + at * Stage<BITS>::bytes, e, lane);
+      if constexpr (BITS == 8) r.ms = scale.x, r.vs = scale.y;
+      __syncwarp();   // and has been read: the stage may be filled again
+      update_block<true, BITS>(r, e, b0 + (long long)i * kTile, lane, s);
+      scale = ahead;
+      at = at + 1 == N ? 0 : at + 1;
+      to = to + 1 == N ? 0 : to + 1;
+    }
+    b0 += (long long)blocks * kTile;
+  }
+  for (; b0 < end; b0 += kTile) {
+    Raw<BITS> r;
+    load_single<BITS>(r, e, b0, lane);
+    update_block<false, BITS>(r, e, b0, lane, s);
+  }
+}
+
 // A block of threads takes a run of consecutive tiles: it looks its first
 // tensor up and walks on from there.
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 adamw_kernel(const __grid_constant__ Table tab, int ntensors, unsigned ntiles, unsigned per_block, Hyper h,
              int last_launch) {
+  extern __shared__ __align__(128) unsigned char staged[];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -296,6 +419,7 @@ adamw_kernel(const __grid_constant__ Table tab, int ntensors, unsigned ntiles, u
   // 1 - beta^t = -expm1(t ln beta): exact to rounding also for the first steps
   s.alpha = lr / expm1f(t * h.lnb1);   // -lr / c1
   s.rc2 = 1.f / sqrtf(-expm1f(t * h.lnb2));
+  const uint32_t stages = (uint32_t)__cvta_generic_to_shared(staged) + warp * kWarpStage;
   const unsigned first = blockIdx.x * per_block, end = min(ntiles, first + per_block);
   int lo = 0;
   if (first < end) {
@@ -305,20 +429,15 @@ adamw_kernel(const __grid_constant__ Table tab, int ntensors, unsigned ntiles, u
       if (tab.e[mid].tile0 <= first) lo = mid; else hi = mid - 1;
     }
   }
-  for (unsigned tile = first; tile < end; ++tile) {
-    while (lo + 1 < ntensors && tab.e[lo + 1].tile0 <= tile) ++lo;
+  for (unsigned tile = first; tile < end; ++lo) {
     const Entry& e = tab.e[lo];
-    const long long b0 = (long long)(tile - e.tile0) * kTile + warp * kBlock;   // the warp's block
-    if (b0 >= e.n) continue;
+    const unsigned stop = lo + 1 < ntensors ? min(end, tab.e[lo + 1].tile0) : end;
     s.keep = 1.f - lr * e.decay;
-    const bool vec = e.vec && b0 + kBlock <= e.n;
-    if (e.bits == 8) {
-      if (vec) update_block<true, 8>(e, b0, lane, s);
-      else update_block<false, 8>(e, b0, lane, s);
-    } else {
-      if (vec) update_block<true, 32>(e, b0, lane, s);
-      else update_block<false, 32>(e, b0, lane, s);
-    }
+    const long long b0 = (long long)(tile - e.tile0) * kTile + warp * kBlock;
+    const long long limit = min(e.n, (long long)(stop - e.tile0) * kTile);
+    if (e.bits == 8) run_tensor<8>(e, b0, limit, stages, lane, s);
+    else run_tensor<32>(e, b0, limit, stages, lane, s);
+    tile = stop;
   }
   if (!last_launch) return;
   // The last block to finish counts the step: by then every block has read it.
@@ -329,12 +448,13 @@ adamw_kernel(const __grid_constant__ Table tab, int ntensors, unsigned ntiles, u
   }
 }
 
-// Every array of the tensor starts on a boundary of eight of its elements.
+// Every array of the tensor allows 16-byte copies and, where it is written, a
+// lane's store of eight elements at once.
 bool vector_aligned(const moe_adamw_tensor& t) {
   auto on = [](const void* p, unsigned bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
-  const unsigned st = t.state_bits == 8 ? 8u : 32u;
-  return on(t.param, 8u * dtype_bytes(t.param_dtype)) && on(t.grad, 8u * dtype_bytes(t.grad_dtype)) &&
-         on(t.master, 32u) && on(t.m, st) && on(t.v, st);
+  const unsigned st = t.state_bits == 8 ? 16u : 32u;
+  return on(t.param, 8u * dtype_bytes(t.param_dtype)) && on(t.grad, 16u) && on(t.master, 32u) && on(t.m, st) &&
+         on(t.v, st);
 }
 
 }  // namespace
@@ -357,6 +477,8 @@ cudaError_t launch_adamw(const moe_adamw_tensor* t, int nt, const moe_adamw_hype
   h.lr_dev = lr_dev;
   h.grad_scale = grad_scale;
   h.state = state;
+  constexpr size_t kSmem = (size_t)kWarpStage * (kThreads / 32);
+  if ((err = set_smem_once<adamw_kernel>(kSmem)) != cudaSuccess) return err;
   Table tab;
   int i = 0;
   do {   // at least one launch: a step over nothing counts, too
@@ -386,7 +508,7 @@ cudaError_t launch_adamw(const moe_adamw_tensor* t, int nt, const moe_adamw_hype
     }
     const unsigned most = (unsigned)di.sms * kBlocksPerSm;
     const unsigned per = std::max(1u, (tiles + most - 1) / most), blocks = std::max(1u, (tiles + per - 1) / per);
-    err = launch_pdl(adamw_kernel, dim3(blocks), dim3(kThreads), 0, s, tab, ne, tiles, per, h, i >= nt ? 1 : 0);
+    err = launch_pdl(adamw_kernel, dim3(blocks), dim3(kThreads), kSmem, s, tab, ne, tiles, per, h, i >= nt ? 1 : 0);
     if (err != cudaSuccess) return err;
   } while (i < nt);
   return cudaSuccess;
