@@ -429,6 +429,8 @@ moe_status moe_aux_coef_next(float coef, float drop_rate, float beta, float xi, 
  *   gradient that reaches h past the norm; dx[rows, d] (may be dsum itself, or
  *   dy when dy_dtype is dx_dtype); dgamma[d], dbeta[d] fp32 or NULL, fully written
  *   (zeros when rows is 0), summed in a fixed order.
+ *   stats: device moe_stats or NULL; a bounded wait that gave up sets
+ *   MOE_DEV_TIMEOUT in status.
  *   ws: moe_layer_norm_workspace_size(cfg) bytes; not read when dgamma and
  *   dbeta are both NULL.
  */
@@ -444,7 +446,7 @@ moe_status moe_layer_norm_forward(const moe_norm_config* cfg, const void* x, con
                                   moe_stream_t stream);
 moe_status moe_layer_norm_backward(const moe_norm_config* cfg, const void* dy, const void* x, const float* mean,
                                    const float* rstd, const void* gamma, const void* dsum, void* dx, float* dgamma,
-                                   float* dbeta, void* ws, size_t ws_bytes, moe_stream_t stream);
+                                   float* dbeta, moe_stats* stats, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
  * The layer with its router's scores in the open, for a loss on them:

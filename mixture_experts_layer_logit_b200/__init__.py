@@ -159,7 +159,7 @@ def lib() -> ctypes.CDLL:
     L.moe_layer_norm_workspace_size.argtypes = [normp]
     L.moe_layer_norm_workspace_size.restype = ctypes.c_size_t
     L.moe_layer_norm_forward.argtypes = [normp] + [P] * 9
-    L.moe_layer_norm_backward.argtypes = [normp] + [P] * 10 + [ctypes.c_size_t, P]
+    L.moe_layer_norm_backward.argtypes = [normp] + [P] * 11 + [ctypes.c_size_t, P]
     L.moe_route_scores.argtypes = [cfgp, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
     L.moe_layer_forward_scores.argtypes = [cfgp, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
     L.moe_layer_backward_scores.argtypes = [cfgp, P, P, P, P, P, P, P, f32, f32, P, ctypes.c_size_t, P, P, P, P, P, P,
@@ -430,6 +430,10 @@ def _arg(fn: str, name: str, t, dev: int, dtype, n: int) -> Optional[int]:
     return t.data_ptr()
 
 
+def _stats(fn: str, stats, dev: int) -> Optional[int]:
+    return None if stats is None else _arg(fn, "stats", stats, dev, stats.dtype, STATS_BYTES // stats.element_size())
+
+
 def _workspace(fn: str, ws, dev: int):
     """(pointer, bytes) of a workspace tensor (None: no workspace)."""
     if ws is None:
@@ -464,7 +468,7 @@ def moe_layer_norm_forward(cfg, x, gamma, beta, y, add=None, sum=None, mean=None
 
 
 def moe_layer_norm_backward(cfg, dy, x, mean, rstd, gamma, dx, dgamma=None, dbeta=None, ws=None, dsum=None,
-                            stream=None):
+                            stats=None, stream=None):
     """dx (of what the forward normalised; dsum is added to it), dgamma, dbeta."""
     fn, dev, n = "moe_layer_norm_backward", _current_device(), cfg.rows * cfg.d
     dxt, f32 = _torch_dtype(cfg.dx_dtype), _torch_dtype(MOE_DTYPE_F32)
@@ -474,7 +478,7 @@ def moe_layer_norm_backward(cfg, dy, x, mean, rstd, gamma, dx, dgamma=None, dbet
         _arg(fn, "x", x, dev, _torch_dtype(cfg.x_dtype), n), _arg(fn, "mean", mean, dev, f32, cfg.rows),
         _arg(fn, "rstd", rstd, dev, f32, cfg.rows), _arg(fn, "gamma", gamma, dev, _torch_dtype(cfg.w_dtype), cfg.d),
         _arg(fn, "dsum", dsum, dev, dxt, n), _arg(fn, "dx", dx, dev, dxt, n),
-        _arg(fn, "dgamma", dgamma, dev, f32, cfg.d), _arg(fn, "dbeta", dbeta, dev, f32, cfg.d), wp, wn,
+        _arg(fn, "dgamma", dgamma, dev, f32, cfg.d), _arg(fn, "dbeta", dbeta, dev, f32, cfg.d), _stats(fn, stats, dev), wp, wn,
         _stream(stream)))
 
 
@@ -537,7 +541,7 @@ def moe_balance_loss(cfg, scores, topk_idx, counts, loss, ws, seq_offsets=None, 
         ctypes.byref(cfg), _arg(fn, "scores", scores, dev, zt, n), ip,
         _arg(fn, "seq_offsets", seq_offsets, dev, i32, cfg.S + 1), _arg(fn, "mask", mask, dev, torch.uint8, cfg.T),
         _arg(fn, "coef", coef, dev, f32, 1), cp, _arg(fn, "loss", loss, dev, f32, 1),
-        _arg(fn, "dscores", dscores, dev, zt, n), _arg(fn, "stats", stats, dev, torch.uint8, STATS_BYTES), wp, wn,
+        _arg(fn, "dscores", dscores, dev, zt, n), _stats(fn, stats, dev), wp, wn,
         _stream(stream)))
 
 

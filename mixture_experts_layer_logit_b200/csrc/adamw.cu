@@ -208,9 +208,6 @@ constexpr int kWarpStage = Stage<8>::bytes * Stage<8>::count > Stage<32>::bytes 
                                ? Stage<8>::bytes * Stage<8>::count
                                : Stage<32>::bytes * Stage<32>::count;
 
-__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
 // 256 elements of type dt, 1024 or 512 bytes
 __device__ __forceinline__ void copy_row(uint32_t to, const void* p, int dt, long long i, int lane) {
   const char* from = static_cast<const char*>(p) + i * (dt == MOE_DTYPE_F32 ? 4 : 2) + lane * 16;
@@ -231,24 +228,21 @@ __device__ __forceinline__ void copy_block(uint32_t st, const Entry& e, long lon
   }
 }
 
-__device__ __forceinline__ void shared8(Raw8& r, uint32_t at, int dt, int lane) {
+__device__ __forceinline__ void shared_row(Raw8& r, uint32_t at, int dt, int lane) {
   at += lane * (dt == MOE_DTYPE_F32 ? 32 : 16);
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "r"(at));
-  if (dt == MOE_DTYPE_F32)
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7]) : "r"(at + 16));
+  shared16(at, r.w[0], r.w[1], r.w[2], r.w[3]);
+  if (dt == MOE_DTYPE_F32) shared16(at + 16, r.w[4], r.w[5], r.w[6], r.w[7]);
 }
 template <int BITS>
 __device__ __forceinline__ void load_staged(Raw<BITS>& r, uint32_t st, const Entry& e, int lane) {
-  shared8(r.g, st + Stage<BITS>::g, e.gdt, lane);
-  shared8(r.p, st + Stage<BITS>::p, e.master != nullptr ? MOE_DTYPE_F32 : e.pdt, lane);
+  shared_row(r.g, st + Stage<BITS>::g, e.gdt, lane);
+  shared_row(r.p, st + Stage<BITS>::p, e.master != nullptr ? MOE_DTYPE_F32 : e.pdt, lane);
   if constexpr (BITS == 8) {
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.m.x), "=r"(r.m.y) : "r"(st + Stage<8>::m + lane * 8));
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.v.x), "=r"(r.v.y) : "r"(st + Stage<8>::v + lane * 8));
+    shared8(st + Stage<8>::m + lane * 8, r.m.x, r.m.y);
+    shared8(st + Stage<8>::v + lane * 8, r.v.x, r.v.y);
   } else {
-    shared8(r.m, st + Stage<32>::m, MOE_DTYPE_F32, lane);
-    shared8(r.v, st + Stage<32>::v, MOE_DTYPE_F32, lane);
+    shared_row(r.m, st + Stage<32>::m, MOE_DTYPE_F32, lane);
+    shared_row(r.v, st + Stage<32>::v, MOE_DTYPE_F32, lane);
   }
 }
 
@@ -373,15 +367,15 @@ __device__ __forceinline__ void run_tensor(const Entry& e, long long b0, long lo
 #pragma unroll
     for (int i = 0; i < N - 1; ++i) {
       if (i < blocks) copy_block<BITS>(stages + i * Stage<BITS>::bytes, e, b0 + (long long)i * kTile, lane);
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      copy_commit();
     }
     int at = 0, to = N - 1;
     for (int i = 0; i < blocks; ++i) {
       if (i + N - 1 < blocks)
         copy_block<BITS>(stages + to * Stage<BITS>::bytes, e, b0 + (long long)(i + N - 1) * kTile, lane);
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      copy_commit();
       if (BITS == 8 && i + 1 < blocks) ahead = scales(i + 1);
-      asm volatile("cp.async.wait_group %0;" ::"n"(N - 1) : "memory");
+      copy_wait<N - 1>();
       __syncwarp();   // every lane's part of the block has arrived
       Raw<BITS> r;
       load_staged<BITS>(r, stages + at * Stage<BITS>::bytes, e, lane);

@@ -640,7 +640,7 @@ moe_status moe_layer_norm_forward(const moe_norm_config* cfg, const void* x, con
 
 moe_status moe_layer_norm_backward(const moe_norm_config* cfg, const void* dy, const void* x, const float* mean,
                                    const float* rstd, const void* gamma, const void* dsum, void* dx, float* dgamma,
-                                   float* dbeta, void* ws, size_t ws_bytes, moe_stream_t stream) {
+                                   float* dbeta, moe_stats* stats, void* ws, size_t ws_bytes, moe_stream_t stream) {
   moe_status st = check_norm(cfg);
   if (st != MOE_OK) return st;
   const moe_norm_config& c = *cfg;
@@ -648,7 +648,7 @@ moe_status moe_layer_norm_backward(const moe_norm_config* cfg, const void* dy, c
     return MOE_ERR_ARG;
   if (!aligned_to(dy, c.dy_dtype) || !aligned_to(x, c.x_dtype) || !aligned4(mean) || !aligned4(rstd) ||
       !aligned_to(gamma, c.w_dtype) || !aligned_to(dsum, c.dx_dtype) || !aligned_to(dx, c.dx_dtype) ||
-      !aligned4(dgamma) || !aligned4(dbeta))
+      !aligned4(dgamma) || !aligned4(dbeta) || !aligned4(stats))
     return MOE_ERR_ARG;
   const bool weights = dgamma != nullptr || dbeta != nullptr;
   if (weights && (st = check_ws(ws, ws_bytes, moe_layer_norm_workspace_size(cfg))) != MOE_OK) return st;
@@ -660,8 +660,8 @@ moe_status moe_layer_norm_backward(const moe_norm_config* cfg, const void* dy, c
       if (p != nullptr && cudaMemsetAsync(p, 0, sizeof(float) * (size_t)c.d, s) != cudaSuccess) return MOE_ERR_CUDA;
     return MOE_OK;
   }
-  return cuda_status(launch_norm_bwd(c, dy, x, mean, rstd, gamma, dsum, dx, dgamma, dbeta, static_cast<float*>(ws),
-                                     s));
+  return cuda_status(launch_norm_bwd(c, dy, x, mean, rstd, gamma, dsum, dx, dgamma, dbeta, stats,
+                                     static_cast<float*>(ws), s));
 }
 
 size_t moe_balance_workspace_size(const moe_balance_config* cfg) {

@@ -40,12 +40,7 @@ __device__ __forceinline__ float round_to(float v, int dt) {
   return __half2float(__float2half_rn(v));
 }
 
-// 32 and 16 bytes at once, past L1: every operand of these kernels is used by one thread only
-__device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8]) {
-  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p));
-}
+// 16 bytes at once, past L1: every operand of these kernels is used by one thread only
 __device__ __forceinline__ void load16(const void* p, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
   asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "l"(p));
 }
@@ -55,10 +50,43 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-// Eight consecutive elements from i on, all there and aligned to their size (32 or 16 bytes).
-__device__ __forceinline__ void load8(Raw8& r, const void* p, int dt, size_t i) {
-  if (dt == MOE_DTYPE_F32) load32(static_cast<const float*>(p) + i, r.w);
-  else load16(static_cast<const unsigned short*>(p) + i, r.w[0], r.w[1], r.w[2], r.w[3]);
+// Words q * 4 .. (fp32) or q * 2 .. (16 bits) of r: four consecutive elements
+// from i on, aligned to their size (16 or 8 bytes).
+__device__ __forceinline__ void load4(Raw8& r, int q, const void* p, int dt, size_t i) {
+  if (dt == MOE_DTYPE_F32)
+    load16(static_cast<const float*>(p) + i, r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]);
+  else
+    asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];"
+                 : "=r"(r.w[2 * q]), "=r"(r.w[2 * q + 1]) : "l"(static_cast<const unsigned short*>(p) + i));
+}
+
+__device__ __forceinline__ void load4_cached(Raw8& r, int q, const void* p, int dt, size_t i) {
+  if (dt == MOE_DTYPE_F32) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i));
+    r.w[4 * q] = v.x, r.w[4 * q + 1] = v.y, r.w[4 * q + 2] = v.z, r.w[4 * q + 3] = v.w;
+  } else {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(p) + i));
+    r.w[2 * q] = v.x, r.w[2 * q + 1] = v.y;
+  }
+}
+
+// Asynchronous copies to shared memory, and reads of what they brought.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {   // until at most N of the thread's groups are under way
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void shared16(uint32_t at, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void shared8(uint32_t at, uint32_t& a, uint32_t& b) {
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(at) : "memory");
 }
 
 __device__ __forceinline__ void to_float8(const Raw8& r, int dt, float (&v)[8]) {
@@ -101,6 +129,22 @@ __device__ __forceinline__ void store8(void* p, int dt, size_t i, const float (&
     }
   }
   *reinterpret_cast<uint4*>(static_cast<unsigned short*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void store4(void* p, int dt, size_t i, float a, float b, float c, float d) {
+  if (dt == MOE_DTYPE_F32) {
+    __stcs(reinterpret_cast<float4*>(static_cast<float*>(p) + i), make_float4(a, b, c, d));
+    return;
+  }
+  uint2 w;
+  if (dt == MOE_DTYPE_BF16) {
+    const __nv_bfloat162 l = __floats2bfloat162_rn(a, b), h = __floats2bfloat162_rn(c, d);
+    w = make_uint2(*reinterpret_cast<const uint32_t*>(&l), *reinterpret_cast<const uint32_t*>(&h));
+  } else {
+    const __half2 l = __floats2half2_rn(a, b), h = __floats2half2_rn(c, d);
+    w = make_uint2(*reinterpret_cast<const uint32_t*>(&l), *reinterpret_cast<const uint32_t*>(&h));
+  }
+  __stcs(reinterpret_cast<uint2*>(static_cast<unsigned short*>(p) + i), w);
 }
 
 }  // namespace moe

@@ -215,7 +215,7 @@ cudaError_t launch_norm_fwd(const moe_norm_config& c, const void* x, const void*
                             const void* beta, void* y, void* sum, float* mean, float* rstd, cudaStream_t s);
 cudaError_t launch_norm_bwd(const moe_norm_config& c, const void* dy, const void* x, const float* mean,
                             const float* rstd, const void* gamma, const void* dsum, void* dx, float* dgamma,
-                            float* dbeta, float* part, cudaStream_t s);
+                            float* dbeta, moe_stats* stats, float* part, cudaStream_t s);
 
 // Byte offsets in the balance loss's workspace: [0, part) is zeroed by the call.
 struct BalanceLayout {

@@ -14,239 +14,249 @@
 // values (two passes over registers, not sums of squares, which cancel when
 // the mean is large).  Sums are fp32.
 #include "elem8.cuh"
+#include "tc_ptx.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 namespace {
 
-constexpr int kMaxWarps = 32;
+constexpr int kMaxWarps = 16;   // of a block
+constexpr int kMaxStages = 4;   // of the backward's ring
 
-// Columns of a thread, eight in each of its NC chunks; t of tpr threads own a
-// row.  VEC (the width and every operand allow vector loads of eight elements):
-// consecutive ones; else strided by tpr, loaded one by one.
-template <bool VEC>
+// How a thread sees a row.  Its columns are eight in each of its NC chunks; t of
+// tpr threads own a row.  kSingle: strided by tpr, one by one.  kVector (the
+// width and every operand allow vectors of four elements): two runs of four,
+// each a whole line over a warp.  kWhole: the same, and every column exists.
+enum Mode { kSingle, kVector, kWhole };
+
+struct Geometry {
+  int rows, d, tpr, groups;   // groups of tpr threads in a block, a row each
+  unsigned magic;             // ceil(2^16 / tpr): threadIdx / tpr without a division
+  float fd, inv_d;
+};
+
+struct Place {
+  int group, t;
+  __device__ __forceinline__ explicit Place(const Geometry& G) {
+    group = G.groups == 1 ? 0 : (int)((threadIdx.x * G.magic) >> 16);
+    t = threadIdx.x - group * G.tpr;
+  }
+};
+
+template <Mode M>
 __device__ __forceinline__ int column(int j, int i, int t, int tpr) {
-  return VEC ? (j * tpr + t) * 8 + i : (j * 8 + i) * tpr + t;
+  return M != kSingle ? ((2 * j + i / 4) * tpr + t) * 4 + (i & 3) : (j * 8 + i) * tpr + t;
+}
+template <Mode M>
+__device__ __forceinline__ bool inside(int c, int d) {
+  return M == kWhole || c < d;
 }
 
-// The raw elements of chunk j of the row that starts at base (zeros past the width).
-template <bool VEC>
+// The raw elements of chunk j of the row that starts at base (zeros past the
+// width).  WEIGHTS: gamma or beta, which every row reads again and L1 keeps.
+template <Mode M, bool WEIGHTS = false>
 __device__ __forceinline__ void load_chunk(Raw8& r, const void* p, int dt, size_t base, int j, int t, int tpr, int d) {
-  if constexpr (VEC) {
-    const int c = column<true>(j, 0, t, tpr);
-    if (c < d) {
-      load8(r, p, dt, base + c);
-    } else {
+  if constexpr (M != kWhole) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) r.w[i] = 0u;
+    for (int i = 0; i < 8; ++i) r.w[i] = 0u;
+  }
+  if constexpr (M != kSingle) {
+    const int c = column<M>(j, 0, t, tpr), c2 = column<M>(j, 4, t, tpr);
+    auto quad = [&](int q, int type, int col) {
+      if constexpr (WEIGHTS) load4_cached(r, q, p, type, col);
+      else load4(r, q, p, type, base + col);
+    };
+    if (dt == MOE_DTYPE_F32) {
+      if (inside<M>(c, d)) quad(0, MOE_DTYPE_F32, c);
+      if (inside<M>(c2, d)) quad(1, MOE_DTYPE_F32, c2);
+    } else {
+      if (inside<M>(c, d)) quad(0, MOE_DTYPE_BF16, c);
+      if (inside<M>(c2, d)) quad(1, MOE_DTYPE_BF16, c2);
     }
   } else {
+    if (dt == MOE_DTYPE_F32) {
+      const uint32_t* f = static_cast<const uint32_t*>(p) + base;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = column<false>(j, i, t, tpr);
-      r.w[i] = c < d ? load_raw1(p, dt, base + c) : 0u;
+      for (int i = 0; i < 8; ++i)
+        if (column<M>(j, i, t, tpr) < d) r.w[i] = f[column<M>(j, i, t, tpr)];
+    } else {
+      const unsigned short* f = static_cast<const unsigned short*>(p) + base;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (column<M>(j, i, t, tpr) < d) r.w[i] = f[column<M>(j, i, t, tpr)];
     }
   }
 }
-template <bool VEC>
+template <Mode M>
 __device__ __forceinline__ void chunk_to_float(const Raw8& r, int dt, float (&v)[8]) {
-  if constexpr (VEC) {
+  if constexpr (M != kSingle) {
     to_float8(r, dt, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = raw_to_float(r.w[i], dt);
   }
 }
-template <bool VEC>
+template <Mode M>
 __device__ __forceinline__ void store_chunk(void* p, int dt, size_t base, int j, int t, int tpr, int d,
                                             const float (&v)[8]) {
-  if constexpr (VEC) {
-    const int c = column<true>(j, 0, t, tpr);
-    if (c < d) store8(p, dt, base + c, v);
-  } else {
+  auto as = [&](int type) {
+    if constexpr (M != kSingle) {
+      const int c = column<M>(j, 0, t, tpr), c2 = column<M>(j, 4, t, tpr);
+      if (inside<M>(c, d)) store4(p, type, base + c, v[0], v[1], v[2], v[3]);
+      if (inside<M>(c2, d)) store4(p, type, base + c2, v[4], v[5], v[6], v[7]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = column<false>(j, i, t, tpr);
-      if (c < d) store1(p, dt, base + c, v[i]);
+      for (int i = 0; i < 8; ++i)
+        if (column<M>(j, i, t, tpr) < d) store1(p, type, base + column<M>(j, i, t, tpr), v[i]);
     }
-  }
+  };
+  if (dt == MOE_DTYPE_F32) as(MOE_DTYPE_F32);
+  else if (dt == MOE_DTYPE_BF16) as(MOE_DTYPE_BF16);
+  else as(MOE_DTYPE_F16);
 }
 
-// Sum over the tpr threads of a row: lanes of a warp (a power of two up to 32)
-// or whole warps (tpr a multiple of 32).  buf: one float2 per warp of the block.
-__device__ __forceinline__ float2 row_sum(float2 v, int tpr, float2* buf) {
-  const int width = tpr < 32 ? tpr : 32;
-  for (int o = width / 2; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-  }
+// Sums over the tpr threads of a row: lanes of a warp (a power of two up to 32)
+// or up to 16 whole warps (tpr a multiple of 32), whose partials meet in buf
+// (one entry per warp of the block) and are added by every warp for itself.
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 from_lane(float2 v, int o) {
+  return make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o));
+}
+__device__ __forceinline__ float from_lane(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+
+template <typename T>
+__device__ __forceinline__ T row_sum(T v, int tpr, int group, T* buf) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < tpr) v = add(v, from_lane(v, o));
   if (tpr > 32) {
-    const int warp = threadIdx.x >> 5, wpr = tpr >> 5, first = warp / wpr * wpr;
-    if ((threadIdx.x & 31) == 0) buf[warp] = v;
+    const int lane = threadIdx.x & 31, wpr = tpr >> 5;
+    if (lane == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = make_float2(0.f, 0.f);
-    for (int w = 0; w < wpr; ++w) {
-      v.x += buf[first + w].x;
-      v.y += buf[first + w].y;
-    }
+    v = T{};
+    if ((lane & 15) < wpr) v = buf[group * wpr + (lane & 15)];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = add(v, from_lane(v, o));
   }
   return v;
 }
 
-template <int NC, bool VEC>
-__global__ void norm_fwd_kernel(const void* x, const void* add, const void* gamma, const void* beta, void* y,
-                                void* sum, float* mean_out, float* rstd_out, int rows, int d, float eps, int xdt,
-                                int ydt, int wdt, int adt, int tpr) {
-  __shared__ float2 buf[2][kMaxWarps];
+// s / d rounded to nearest, with inv = 1 / d: the quotient's exact residual corrects it
+__device__ __forceinline__ float over(float s, float d, float inv) {
+  const float q = s * inv;
+  return fmaf(fmaf(-q, d, s), inv, q);
+}
+
+// 1 / sqrt(v) to about an ulp: one Newton step on the approximation
+__device__ __forceinline__ float inverse_root(float v) {
+  const float y = rsqrtf(v);
+  return y * fmaf(-0.5f * v * y, y, 1.5f);
+}
+
+struct NormFwd {
+  Geometry G;
+  const void* x;
+  const void* add;
+  const void* gamma;
+  const void* beta;
+  void* y;
+  void* sum;
+  float* mean;
+  float* rstd;
+  float eps;
+  int xdt, ydt, wdt, adt;
+};
+
+template <int NC, Mode M>
+__global__ void __launch_bounds__(512, NC == 1 ? 3 : NC == 2 ? 2 : 1) norm_fwd_kernel(const NormFwd a) {
+  __shared__ float buf[2][kMaxWarps];
   pdl_wait();
   pdl_launch_dependents();
-  const int g = threadIdx.x / tpr, t = threadIdx.x - g * tpr;
-  const int row = blockIdx.x * (blockDim.x / tpr) + g;
-  const bool live = row < rows;
+  const Place at(a.G);
+  const int tpr = a.G.tpr, d = a.G.d, t = at.t;
+  const int row = blockIdx.x * a.G.groups + at.group;
+  const bool live = row < a.G.rows;
   const size_t base = (size_t)(live ? row : 0) * d;
   Raw8 rx[NC], ra[NC];
 #pragma unroll
-  for (int j = 0; j < NC; ++j) load_chunk<VEC>(rx[j], x, xdt, base, j, t, tpr, d);
-  if (add != nullptr) {
+  for (int j = 0; j < NC; ++j) load_chunk<M>(rx[j], a.x, a.xdt, base, j, t, tpr, d);
+  if (a.add != nullptr) {
 #pragma unroll
-    for (int j = 0; j < NC; ++j) load_chunk<VEC>(ra[j], add, adt, base, j, t, tpr, d);
+    for (int j = 0; j < NC; ++j) load_chunk<M>(ra[j], a.add, a.adt, base, j, t, tpr, d);
   }
-  float h[NC][8];
-  float2 s = make_float2(0.f, 0.f);
+  float h[NC][8], s = 0.f;
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
-    chunk_to_float<VEC>(rx[j], xdt, h[j]);
-    if (add != nullptr) {
-      float a[8];
-      chunk_to_float<VEC>(ra[j], adt, a);
+    chunk_to_float<M>(rx[j], a.xdt, h[j]);
+    if (a.add != nullptr) {
+      float v[8];
+      chunk_to_float<M>(ra[j], a.adt, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[j][i] = round_to(h[j][i] + a[i], xdt);
-      if (sum != nullptr && live) store_chunk<VEC>(sum, xdt, base, j, t, tpr, d, h[j]);
+      for (int i = 0; i < 8; ++i) h[j][i] += v[i];
+      if (a.xdt != MOE_DTYPE_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j][i] = round_to(h[j][i], a.xdt);
+      }
+      if (a.sum != nullptr && live) store_chunk<M>(a.sum, a.xdt, base, j, t, tpr, d, h[j]);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s.x += h[j][i];   // columns past the width hold zeros
+    for (int i = 0; i < 8; ++i) s += h[j][i];   // columns past the width hold zeros
   }
-  const float mu = row_sum(s, tpr, buf[0]).x / (float)d;
-  s = make_float2(0.f, 0.f);
+  const float mu = over(row_sum(s, tpr, at.group, buf[0]), a.G.fd, a.G.inv_d);
+  s = 0.f;
 #pragma unroll
   for (int j = 0; j < NC; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (column<VEC>(j, i, t, tpr) < d) {
-        const float v = h[j][i] - mu;
-        s.x += v * v;
-      }
-  const float rstd = 1.f / sqrtf(row_sum(s, tpr, buf[1]).x / (float)d + eps);
+    for (int i = 0; i < 8; ++i) {
+      h[j][i] -= mu;
+      if (inside<M>(column<M>(j, M == kSingle ? i : i & 4, t, tpr), d)) s += h[j][i] * h[j][i];
+    }
+  const float rstd = inverse_root(over(row_sum(s, tpr, at.group, buf[1]), a.G.fd, a.G.inv_d) + a.eps);
   if (!live) return;
   if (t == 0) {
-    if (mean_out != nullptr) mean_out[row] = mu;
-    if (rstd_out != nullptr) rstd_out[row] = rstd;
+    if (a.mean != nullptr) a.mean[row] = mu;
+    if (a.rstd != nullptr) a.rstd[row] = rstd;
   }
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     Raw8 r;
-    float w[8];
+    float w[8], b[8];
+    if (a.gamma != nullptr) {
+      load_chunk<M, true>(r, a.gamma, a.wdt, 0, j, t, tpr, d);
+      chunk_to_float<M>(r, a.wdt, w);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[j][i] = (h[j][i] - mu) * rstd;
-    if (gamma != nullptr) {
-      load_chunk<VEC>(r, gamma, wdt, 0, j, t, tpr, d);
-      chunk_to_float<VEC>(r, wdt, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[j][i] *= w[i];
+      for (int i = 0; i < 8; ++i) w[i] = 1.f;
     }
-    if (beta != nullptr) {
-      load_chunk<VEC>(r, beta, wdt, 0, j, t, tpr, d);
-      chunk_to_float<VEC>(r, wdt, w);
+    if (a.beta != nullptr) {
+      load_chunk<M, true>(r, a.beta, a.wdt, 0, j, t, tpr, d);
+      chunk_to_float<M>(r, a.wdt, b);
+    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[j][i] += w[i];
+      for (int i = 0; i < 8; ++i) b[i] = 0.f;
     }
-    store_chunk<VEC>(y, ydt, base, j, t, tpr, d, h[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[j][i] = fmaf(h[j][i] * rstd, w[i], b[i]);
+    store_chunk<M>(a.y, a.ydt, base, j, t, tpr, d, h[j]);
   }
 }
 
-// dx of a row at a time; the columns' sums over the block's rows stay with the
-// thread that owns the column and end in part[block][2][d].
-template <int NC, bool VEC>
-__global__ void __launch_bounds__(512)
-norm_bwd_kernel(const void* dy, const void* x, const float* __restrict__ mean, const float* __restrict__ rstd,
-                const void* gamma, const void* dsum, void* dx, float* __restrict__ part, int rows, int d, int xdt,
-                int wdt, int gdt, int odt, int tpr) {
-  __shared__ float2 buf[2][kMaxWarps];
-  extern __shared__ float cols[];   // [groups][2][d] when several rows share the block
-  pdl_wait();
-  pdl_launch_dependents();
-  const int groups = blockDim.x / tpr;
-  const int g = threadIdx.x / tpr, t = threadIdx.x - g * tpr;
-  float dg[NC][8], db[NC][8];
-#pragma unroll
-  for (int j = 0; j < NC; ++j)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dg[j][i] = db[j][i] = 0.f;
-  int turn = 0;
-  for (long long r0 = (long long)blockIdx.x * groups; r0 < rows; r0 += (long long)gridDim.x * groups, turn ^= 1) {
-    const bool live = r0 + g < rows;
-    const long long row = live ? r0 + g : 0;
-    const size_t base = (size_t)row * d;
-    Raw8 rx[NC], ry[NC], rs_[NC];
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      load_chunk<VEC>(ry[j], dy, gdt, base, j, t, tpr, d);
-      load_chunk<VEC>(rx[j], x, xdt, base, j, t, tpr, d);
-    }
-    if (dsum != nullptr) {
-#pragma unroll
-      for (int j = 0; j < NC; ++j) load_chunk<VEC>(rs_[j], dsum, odt, base, j, t, tpr, d);
-    }
-    const float mu = mean[row], rs = rstd[row];
-    float xh[NC][8], gy[NC][8];
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      chunk_to_float<VEC>(rx[j], xdt, xh[j]);
-      chunk_to_float<VEC>(ry[j], gdt, gy[j]);
-      Raw8 r;
-      float w[8];
-      if (gamma != nullptr) {
-        load_chunk<VEC>(r, gamma, wdt, 0, j, t, tpr, d);
-        chunk_to_float<VEC>(r, wdt, w);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        xh[j][i] = (xh[j][i] - mu) * rs;   // of no use past the width, where dy is zero
-        if (live) {
-          dg[j][i] += gy[j][i] * xh[j][i];
-          db[j][i] += gy[j][i];
-        }
-        if (gamma != nullptr) gy[j][i] *= w[i];
-        s.x += gy[j][i];
-        s.y += gy[j][i] * xh[j][i];
-      }
-    }
-    s = row_sum(s, tpr, buf[turn]);
-    const float a = s.x / (float)d, b = s.y / (float)d;
-    if (!live) continue;
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      float w[8];
-      if (dsum != nullptr) chunk_to_float<VEC>(rs_[j], odt, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        xh[j][i] = rs * (gy[j][i] - a - xh[j][i] * b);
-        if (dsum != nullptr) xh[j][i] += w[i];
-      }
-      store_chunk<VEC>(dx, odt, base, j, t, tpr, d, xh[j]);
-    }
-  }
-  if (part == nullptr) return;
+// The block's column sums to part[block][2][d]: cols[groups][2][d] gathers them
+// when several rows share the block.
+template <int NC, Mode M>
+__device__ __forceinline__ void write_columns(const float (&dg)[NC][8], const float (&db)[NC][8], float* cols,
+                                              float* part, int d, int g, int groups, int t, int tpr) {
   float* out = part + (size_t)blockIdx.x * 2 * d;
   float* mine = groups == 1 ? out : cols + (size_t)g * 2 * d;
 #pragma unroll
   for (int j = 0; j < NC; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int c = column<VEC>(j, i, t, tpr);
-      if (c < d) {
+      const int c = column<M>(j, i, t, tpr);
+      if (inside<M>(c, d)) {
         mine[c] = dg[j][i];
         mine[d + c] = db[j][i];
       }
@@ -260,17 +270,265 @@ norm_bwd_kernel(const void* dy, const void* x, const float* __restrict__ mean, c
   }
 }
 
+struct NormBwd {
+  Geometry G;
+  const void* dy;
+  const void* x;
+  const float* mean;
+  const float* rstd;
+  const void* gamma;
+  const void* dsum;
+  void* dx;
+  float* part;
+  int xdt, wdt, gdt, odt;
+  uint32_t* status;
+};
+
+// dx of a row at a time; the columns' sums over the block's rows stay with the
+// thread that owns the column.  The rows of the block's next rounds (one row
+// for each of its groups, which lie one after the other) come by bulk copies
+// of a whole row each, issued by one thread, into a ring of `stages`: the
+// threads spend nothing on loads, and a stage is filled again as soon as every
+// warp has read it.
+template <int NC, Mode M>
+__global__ void __launch_bounds__(512, NC == 1 ? 2 : 1) norm_bwd_rows_kernel(const NormBwd a, int stages) {
+  __shared__ float2 buf[2][kMaxWarps];
+  __shared__ unsigned long long full[kMaxStages], read[kMaxStages];
+  __shared__ int abort_flag;
+  extern __shared__ __align__(128) unsigned char dyn[];   // [stages][dy, x, dsum][groups][d]
+  const Place place(a.G);
+  const int tpr = a.G.tpr, d = a.G.d, rows = a.G.rows, groups = a.G.groups, g = place.group, t = place.t;
+  const uint32_t smem = tc::smem_u32(dyn), bars = tc::smem_u32(full), done = tc::smem_u32(read);
+  const uint32_t row_y = d * (a.gdt == MOE_DTYPE_F32 ? 4 : 2), row_x = d * (a.xdt == MOE_DTYPE_F32 ? 4 : 2);
+  const uint32_t row_s = a.dsum == nullptr ? 0 : d * (a.odt == MOE_DTYPE_F32 ? 4 : 2);
+  const uint32_t stage = groups * (row_y + row_x + row_s);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      tc::mbar_init(bars + 8 * i, 1);
+      tc::mbar_init(done + 8 * i, (blockDim.x + 31) / 32);
+    }
+    abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long step = (long long)gridDim.x * groups;
+  auto fill = [&](int to, long long r0) {   // one thread: the rows from r0 on into stage `to`
+    if (r0 >= rows) return;
+    const uint32_t n = (uint32_t)min((long long)groups, rows - r0), bar = bars + 8 * to;
+    uint32_t at = smem + to * stage;
+    tc::mbar_expect_tx(bar, n * (row_y + row_x + row_s));
+    tc::bulk_load(at, static_cast<const char*>(a.dy) + r0 * row_y, n * row_y, bar);
+    at += groups * row_y;
+    tc::bulk_load(at, static_cast<const char*>(a.x) + r0 * row_x, n * row_x, bar);
+    at += groups * row_x;
+    if (row_s != 0) tc::bulk_load(at, static_cast<const char*>(a.dsum) + r0 * row_s, n * row_s, bar);
+  };
+  __syncthreads();
+  const long long first = (long long)blockIdx.x * groups;
+  long long r0 = first;
+  if (threadIdx.x == 0)
+    for (int i = 0; i < stages; ++i) fill(i, r0 + i * step);
+  // eight elements of the row that starts at `from`, chunk j
+  auto fetch = [&](float (&v)[8], uint32_t from, int dt, int j) {
+    Raw8 r;
+    const int c = column<M>(j, 0, t, tpr), c2 = column<M>(j, 4, t, tpr);
+    if constexpr (M != kWhole) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r.w[i] = 0u;
+    }
+    if (dt == MOE_DTYPE_F32) {
+      if (inside<M>(c, d)) shared16(from + c * 4, r.w[0], r.w[1], r.w[2], r.w[3]);
+      if (inside<M>(c2, d)) shared16(from + c2 * 4, r.w[4], r.w[5], r.w[6], r.w[7]);
+    } else {
+      if (inside<M>(c, d)) shared8(from + c * 2, r.w[0], r.w[1]);
+      if (inside<M>(c2, d)) shared8(from + c2 * 2, r.w[2], r.w[3]);
+    }
+    to_float8(r, dt, v);
+  };
+  float w[NC][8], dg[NC][8], db[NC][8];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    if (a.gamma != nullptr) {
+      Raw8 r;
+      load_chunk<M, true>(r, a.gamma, a.wdt, 0, j, t, tpr, d);
+      to_float8(r, a.wdt, w[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (a.gamma == nullptr) w[j][i] = 1.f;
+      dg[j][i] = db[j][i] = 0.f;
+    }
+  }
+  float mu = 0.f, rs = 0.f;
+  if (r0 + g < rows) mu = a.mean[r0 + g], rs = a.rstd[r0 + g];
+  int turn = 0, at = 0, drains = stages;
+  uint32_t phase = 0;
+  for (; r0 < rows; r0 += step, turn ^= 1) {
+    const long long row = r0 + g;
+    const bool live = row < rows;
+    float mu_next = 0.f, rs_next = 0.f;
+    if (row + step < rows) mu_next = a.mean[row + step], rs_next = a.rstd[row + step];
+    // a wait that runs out: the status says so, no more copies are issued, and
+    // those under way are given a little longer
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (tc::mbar_try_wait(bar, parity) || tc::mbar_wait(bar, parity, &abort_flag, tc::kWaitNs)) return true;
+      abort_flag = 1;
+      if (a.status != nullptr) atomicOr(a.status, MOE_DEV_TIMEOUT);
+      if (drains-- > 0) tc::mbar_wait(bar, parity, nullptr, tc::kDrainNs);
+      return false;
+    };
+    if (threadIdx.x == 0 && r0 != first) {   // the stage of the round before
+      const int to = at == 0 ? stages - 1 : at - 1;
+      if (wait(done + 8 * to, at == 0 ? phase ^ 1 : phase)) fill(to, r0 + (stages - 1) * step);
+    }
+    wait(bars + 8 * at, phase);
+    const uint32_t from = smem + at * stage + g * row_y;
+    const uint32_t from_x = smem + at * stage + groups * row_y + g * row_x;
+    float xh[NC][8], gy[NC][8];
+    float2 s = make_float2(0.f, 0.f);
+    if (live) {
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        fetch(gy[j], from, a.gdt, j);
+        fetch(xh[j], from_x, a.xdt, j);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          xh[j][i] = (xh[j][i] - mu) * rs;   // of no use past the width, where dy is zero
+          dg[j][i] += gy[j][i] * xh[j][i];
+          db[j][i] += gy[j][i];
+          gy[j][i] *= w[j][i];
+          s.x += gy[j][i];
+          s.y += gy[j][i] * xh[j][i];
+        }
+      }
+    }
+    s = row_sum(s, tpr, g, buf[turn]);
+    if (live) {
+      const float r1 = -rs * s.x * a.G.inv_d, r2 = -rs * s.y * a.G.inv_d;
+      const uint32_t from_s = smem + at * stage + groups * (row_y + row_x) + g * row_s;
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xh[j][i] = fmaf(xh[j][i], r2, fmaf(gy[j][i], rs, r1));
+        if (a.dsum != nullptr) {
+          float v[8];
+          fetch(v, from_s, a.odt, j);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) xh[j][i] += v[i];
+        }
+        store_chunk<M>(a.dx, a.odt, (size_t)row * d, j, t, tpr, d, xh[j]);
+      }
+    }
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(done + 8 * at);
+    mu = mu_next, rs = rs_next;
+    if (++at == stages) at = 0, phase ^= 1;
+  }
+  if (a.part == nullptr) return;
+  __syncthreads();   // the stages are free: the columns of the block's rows meet there
+  write_columns<NC, M>(dg, db, reinterpret_cast<float*>(dyn), a.part, d, g, groups, t, tpr);
+}
+
+// The same with plain loads, for widths and pointers without vectors and for
+// rows too wide to keep: those (NC = 4) are read a second time, from L2.
+template <int NC, Mode M>
+__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwd a) {
+  constexpr bool KEEP = NC <= 2;
+  __shared__ float2 buf[2][kMaxWarps];
+  extern __shared__ __align__(16) unsigned char dyn[];
+  pdl_wait();
+  pdl_launch_dependents();
+  const Place place(a.G);
+  const int tpr = a.G.tpr, d = a.G.d, rows = a.G.rows, groups = a.G.groups, g = place.group, t = place.t;
+  float dg[NC][8], db[NC][8], xh[KEEP ? NC : 1][8], gy[KEEP ? NC : 1][8];
+#pragma unroll
+  for (int j = 0; j < NC; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dg[j][i] = db[j][i] = 0.f;
+  const float inv_d = a.G.inv_d;
+  int turn = 0;
+  for (long long r0 = (long long)blockIdx.x * groups; r0 < rows; r0 += (long long)gridDim.x * groups, turn ^= 1) {
+    const bool live = r0 + g < rows;
+    const long long row = live ? r0 + g : 0;
+    const size_t base = (size_t)row * d;
+    const float mu = a.mean[row], rs = a.rstd[row];
+    // chunk j of the row: xh and dy into xh[k], gy[k]; then gamma into dy
+    auto read = [&](int j, int k) {
+      Raw8 ry, rx;
+      load_chunk<M>(ry, a.dy, a.gdt, base, j, t, tpr, d);
+      load_chunk<M>(rx, a.x, a.xdt, base, j, t, tpr, d);
+      chunk_to_float<M>(ry, a.gdt, gy[k]);
+      chunk_to_float<M>(rx, a.xdt, xh[k]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xh[k][i] = (xh[k][i] - mu) * rs;   // of no use past the width, where dy is zero
+    };
+    auto weigh = [&](int j, int k) {
+      if (a.gamma == nullptr) return;
+      Raw8 r;
+      float w[8];
+      load_chunk<M, true>(r, a.gamma, a.wdt, 0, j, t, tpr, d);
+      chunk_to_float<M>(r, a.wdt, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) gy[k][i] *= w[i];
+    };
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int k = KEEP ? j : 0;
+      read(j, k);
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dg[j][i] += gy[k][i] * xh[k][i];
+          db[j][i] += gy[k][i];
+        }
+      }
+      weigh(j, k);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s.x += gy[k][i];
+        s.y += gy[k][i] * xh[k][i];
+      }
+    }
+    s = row_sum(s, tpr, g, buf[turn]);
+    const float m1 = s.x * inv_d, m2 = s.y * inv_d;
+    if (!live) continue;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int k = KEEP ? j : 0;
+      if (!KEEP) {
+        read(j, k);
+        weigh(j, k);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xh[k][i] = rs * (gy[k][i] - m1 - xh[k][i] * m2);
+      if (a.dsum != nullptr) {
+        Raw8 r;
+        float v[8];
+        load_chunk<M>(r, a.dsum, a.odt, base, j, t, tpr, d);
+        chunk_to_float<M>(r, a.odt, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xh[k][i] += v[i];
+      }
+      store_chunk<M>(a.dx, a.odt, base, j, t, tpr, d, xh[k]);
+    }
+  }
+  if (a.part == nullptr) return;
+  write_columns<NC, M>(dg, db, reinterpret_cast<float*>(dyn), a.part, d, g, groups, t, tpr);
+}
+
 // dgamma and dbeta: the blocks' partial sums of each column.  A block takes 32
-// columns; its eight warps each add a run of the parts, and the runs are added
+// columns; its 32 warps each add a run of the parts, and the runs are added
 // in order.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
 norm_weights_kernel(const float* __restrict__ part, int nparts, int d, float* dgamma, float* dbeta) {
-  __shared__ float runs[8][32];
+  __shared__ float runs[32][33];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
-  const int p0 = (int)((long long)nparts * warp / 8), p1 = (int)((long long)nparts * (warp + 1) / 8);
+  const int p0 = (int)((long long)nparts * warp / 32), p1 = (int)((long long)nparts * (warp + 1) / 32);
   float v = 0.f;
   if (c < 2 * d) {
 #pragma unroll 8
@@ -280,7 +538,8 @@ norm_weights_kernel(const float* __restrict__ part, int nparts, int d, float* dg
   __syncthreads();
   if (warp != 0 || c >= 2 * d) return;
   v = 0.f;
-  for (int w = 0; w < 8; ++w) v += runs[w][lane];
+#pragma unroll
+  for (int w = 0; w < 32; ++w) v += runs[w][lane];
   if (c < d) {
     if (dgamma != nullptr) dgamma[c] = v;
   } else if (dbeta != nullptr) {
@@ -288,69 +547,125 @@ norm_weights_kernel(const float* __restrict__ part, int nparts, int d, float* dg
   }
 }
 
-// The width and a pointer allow vector accesses of eight elements.
-bool vector_width(int d) { return d % 8 == 0; }
-bool on_vector(const void* p, int dt) { return reinterpret_cast<uintptr_t>(p) % (8u * dtype_bytes(dt)) == 0; }
+// The width and a pointer allow vector accesses of four elements.
+bool vector_width(int d) { return d % 4 == 0; }
+bool on_vector(const void* p, int dt) { return reinterpret_cast<uintptr_t>(p) % (4u * dtype_bytes(dt)) == 0; }
 
-// Threads of a row, eight elements each or more: a power of two inside a warp, else whole warps up to `most`.
-int threads_per_row(int d, int most) {
+// How a row is spread over threads: tpr of them with nc chunks of eight columns
+// each.  Up to 64 chunks stay inside a warp (no barrier); above, one chunk a
+// thread as long as 512 threads reach, then two and four.
+struct Shape {
+  int tpr, nc, threads, groups;
+};
+Shape shape_of(int d) {
   const int chunks = (d + 7) / 8;
+  Shape s;
   if (chunks <= 32) {
-    int t = 1;
-    while (t < chunks) t *= 2;
-    return t;
+    s.tpr = 1;
+    while (s.tpr < chunks) s.tpr *= 2;
+    s.nc = 1;
+  } else if (chunks <= 64) {
+    s.tpr = 32;
+    s.nc = 2;
+  } else {
+    s.nc = chunks <= 1024 ? 2 : 4;
+    s.tpr = ((chunks + s.nc - 1) / s.nc + 31) / 32 * 32;
   }
-  return std::min(most, (chunks + 31) / 32 * 32);
+  s.groups = std::max(1, 256 / s.tpr);
+  s.threads = s.groups * s.tpr;
+  return s;
+}
+
+Geometry geometry(const moe_norm_config& c, const Shape& s) {
+  return Geometry{c.rows,   c.d, s.tpr, s.groups, (unsigned)((65536 + s.tpr - 1) / s.tpr),
+                  (float)c.d, 1.f / (float)c.d};
+}
+
+template <typename F>
+cudaError_t with_mode(bool vec, const Shape& s, int d, F&& f) {
+  if (!vec) return f(std::integral_constant<Mode, kSingle>{});
+  if (8 * s.nc * s.tpr == d) return f(std::integral_constant<Mode, kWhole>{});
+  return f(std::integral_constant<Mode, kVector>{});
+}
+
+// Blocks of the backward that an SM holds at once: 64 registers a thread with
+// one chunk, else 128.
+int bwd_resident(const Shape& s) { return std::max(1, (s.nc == 1 ? 1024 : 512) / s.threads); }
+
+// Blocks of the backward: what 148 SMs hold at once, rounds of rows shared out evenly.
+int bwd_blocks(const moe_norm_config& c, const Shape& s) {
+  const long long rounds = std::max<long long>(1, ((long long)c.rows + s.groups - 1) / s.groups);
+  const long long most = 148LL * bwd_resident(s);
+  const long long per = (rounds + most - 1) / most;
+  return (int)((rounds + per - 1) / per);
+}
+
+// Rows that bulk copies can bring: whole 16-byte pieces from 16-byte boundaries.
+bool bulk_rows(const void* p, int dt, int d) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (size_t)d * dtype_bytes(dt) % 16 == 0;
 }
 
 }  // namespace
 
-// Blocks of the backward, each of which leaves one partial of the weights' gradient.
-int norm_bwd_blocks(const moe_norm_config& c) {
-  const int tpr = threads_per_row(c.d, 512), groups = std::max(1, 256 / tpr);
-  return (int)std::max<long long>(1, std::min<long long>(((long long)c.rows + groups - 1) / groups, 2 * 148));
-}
+// Each block leaves one partial of the weights' gradient.
+int norm_bwd_blocks(const moe_norm_config& c) { return bwd_blocks(c, shape_of(c.d)); }
 
 cudaError_t launch_norm_fwd(const moe_norm_config& c, const void* x, const void* add, const void* gamma,
                             const void* beta, void* y, void* sum, float* mean, float* rstd, cudaStream_t s) {
-  const int tpr = threads_per_row(c.d, 512), nc = ((c.d + 7) / 8 + tpr - 1) / tpr;
-  const int threads = std::max(tpr, 256 / tpr * tpr), groups = threads / tpr;
-  const dim3 grid((unsigned)(((long long)c.rows + groups - 1) / groups));
+  const Shape sh = shape_of(c.d);
   const bool vec = vector_width(c.d) && on_vector(x, c.x_dtype) && on_vector(add, c.add_dtype) &&
                    on_vector(gamma, c.w_dtype) && on_vector(beta, c.w_dtype) && on_vector(y, c.y_dtype) &&
                    on_vector(sum, c.x_dtype);
-  auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, dim3(threads), 0, s, x, add, gamma, beta, y, sum, mean, rstd, c.rows, c.d, c.eps,
-                      c.x_dtype, c.y_dtype, c.w_dtype, c.add_dtype, tpr);
-  };
-  if (vec)
-    return nc == 1 ? go(norm_fwd_kernel<1, true>) : nc == 2 ? go(norm_fwd_kernel<2, true>) : go(norm_fwd_kernel<4, true>);
-  return nc == 1 ? go(norm_fwd_kernel<1, false>)
-                 : nc == 2 ? go(norm_fwd_kernel<2, false>) : go(norm_fwd_kernel<4, false>);
+  const NormFwd a{geometry(c, sh), x,     add,       gamma,     beta,      y,
+                  sum,             mean,  rstd,      c.eps,     c.x_dtype, c.y_dtype,
+                  c.w_dtype,       c.add_dtype};
+  const dim3 grid((unsigned)(((long long)c.rows + sh.groups - 1) / sh.groups));
+  return with_mode(vec, sh, c.d, [&](auto mode) {
+    constexpr Mode M = decltype(mode)::value;
+    auto kernel = sh.nc == 1 ? norm_fwd_kernel<1, M> : sh.nc == 2 ? norm_fwd_kernel<2, M> : norm_fwd_kernel<4, M>;
+    return launch_pdl(kernel, grid, dim3(sh.threads), 0, s, a);
+  });
 }
 
 cudaError_t launch_norm_bwd(const moe_norm_config& c, const void* dy, const void* x, const float* mean,
                             const float* rstd, const void* gamma, const void* dsum, void* dx, float* dgamma,
-                            float* dbeta, float* part, cudaStream_t s) {
-  const int tpr = threads_per_row(c.d, 512), nc = ((c.d + 7) / 8 + tpr - 1) / tpr;
-  const int threads = std::max(tpr, 256 / tpr * tpr), groups = threads / tpr, blocks = norm_bwd_blocks(c);
-  float* partials = dgamma != nullptr || dbeta != nullptr ? part : nullptr;
-  // several groups have tpr <= 128 threads of one chunk: at most 16 KB
-  const size_t smem = groups > 1 && partials != nullptr ? (size_t)groups * 2 * c.d * sizeof(float) : 0;
-  auto go = [&](auto kernel) {
-    return launch_pdl(kernel, dim3(blocks), dim3(threads), smem, s, dy, x, mean, rstd, gamma, dsum, dx, partials,
-                      c.rows, c.d, c.x_dtype, c.w_dtype, c.dy_dtype, c.dx_dtype, tpr);
-  };
+                            float* dbeta, moe_stats* stats, float* part, cudaStream_t s) {
+  const Shape sh = shape_of(c.d);
+  const bool weights = dgamma != nullptr || dbeta != nullptr;
+  const NormBwd a{geometry(c, sh),          dy,        x,         mean,       rstd,       gamma, dsum, dx,
+                  weights ? part : nullptr, c.x_dtype, c.w_dtype, c.dy_dtype, c.dx_dtype,
+                  stats != nullptr ? &stats->status : nullptr};
+  // the columns of several rows in a block: groups * d <= 256 * 16, at most 32 KB
+  const size_t cols = sh.groups > 1 && weights ? (size_t)sh.groups * 2 * c.d * sizeof(float) : 0;
   const bool vec = vector_width(c.d) && on_vector(dy, c.dy_dtype) && on_vector(x, c.x_dtype) &&
                    on_vector(gamma, c.w_dtype) && on_vector(dsum, c.dx_dtype) && on_vector(dx, c.dx_dtype);
-  cudaError_t e;
-  if (vec)
-    e = nc == 1 ? go(norm_bwd_kernel<1, true>) : nc == 2 ? go(norm_bwd_kernel<2, true>) : go(norm_bwd_kernel<4, true>);
-  else
-    e = nc == 1 ? go(norm_bwd_kernel<1, false>)
-                : nc == 2 ? go(norm_bwd_kernel<2, false>) : go(norm_bwd_kernel<4, false>);
-  if (e != cudaSuccess || partials == nullptr) return e;
-  return launch_pdl(norm_weights_kernel, dim3((2 * c.d + 31) / 32), dim3(256), 0, s, (const float*)part, blocks,
+  const bool bulk = vec && sh.nc <= 2 && bulk_rows(dy, c.dy_dtype, c.d) && bulk_rows(x, c.x_dtype, c.d) &&
+                    (dsum == nullptr || bulk_rows(dsum, c.dx_dtype, c.d));
+  // a ring of two to four rounds of rows in the block's share of an SM's shared memory
+  const size_t round = (size_t)sh.groups * c.d * (dtype_bytes(c.dy_dtype) + dtype_bytes(c.x_dtype) +
+                                                  (dsum != nullptr ? dtype_bytes(c.dx_dtype) : 0));
+  const size_t share = (size_t)(220 << 10) / bwd_resident(sh) - (2 << 10);
+  const int stages = (int)std::min<size_t>(kMaxStages, share / round);
+  const int blocks = bwd_blocks(c, sh);
+  const cudaError_t e = with_mode(vec, sh, c.d, [&](auto mode) {
+    constexpr Mode M = decltype(mode)::value;
+    cudaError_t err;
+    if constexpr (M != kSingle) {
+      if (bulk && stages >= 2) {
+        const size_t smem = std::max(stages * round, cols);
+        auto rows = [&](auto kernel) { return launch_pdl(kernel, dim3(blocks), dim3(sh.threads), smem, s, a, stages); };
+        if (sh.nc == 1)
+          return (err = set_smem_once<norm_bwd_rows_kernel<1, M>>(220 << 10)) != cudaSuccess
+                     ? err : rows(norm_bwd_rows_kernel<1, M>);
+        return (err = set_smem_once<norm_bwd_rows_kernel<2, M>>(220 << 10)) != cudaSuccess
+                   ? err : rows(norm_bwd_rows_kernel<2, M>);
+      }
+    }
+    return launch_pdl(sh.nc == 1 ? norm_bwd_kernel<1, M> : sh.nc == 2 ? norm_bwd_kernel<2, M> : norm_bwd_kernel<4, M>,
+                      dim3(blocks), dim3(sh.threads), cols, s, a);
+  });
+  if (e != cudaSuccess || !weights) return e;
+  return launch_pdl(norm_weights_kernel, dim3((2 * c.d + 31) / 32), dim3(1024), 0, s, (const float*)part, blocks,
                     c.d, dgamma, dbeta);
 }
 

@@ -29,9 +29,10 @@ def fwd(L, c, x=P, add=None, gamma=P, beta=P, y=P, sum=None, mean=P, rstd=P):
     return L.moe_layer_norm_forward(BY(c) if c else None, x, add, gamma, beta, y, sum, mean, rstd, None)
 
 
-def bwd(L, c, dy=P, x=P, mean=P, rstd=P, gamma=P, dsum=None, dx=P, dgamma=P, dbeta=P, ws=P, n=1 << 30):
-    return L.moe_layer_norm_backward(BY(c) if c else None, dy, x, mean, rstd, gamma, dsum, dx, dgamma, dbeta, ws, n,
-                                     None)
+def bwd(L, c, dy=P, x=P, mean=P, rstd=P, gamma=P, dsum=None, dx=P, dgamma=P, dbeta=P, stats=None, ws=P,
+        n=1 << 30):
+    return L.moe_layer_norm_backward(BY(c) if c else None, dy, x, mean, rstd, gamma, dsum, dx, dgamma, dbeta, stats,
+                                     ws, n, None)
 
 
 def test_struct_sizes(L):
@@ -66,7 +67,7 @@ def test_norm_pointers(L):
     assert fwd(L, c, add=P, sum=P + 2) == 1
     for name in ("dy", "x", "mean", "rstd", "dx"):
         assert bwd(L, c, **{name: None}) == 1, name
-    for name in ("dy", "x", "mean", "rstd", "gamma", "dsum", "dx", "dgamma", "dbeta"):
+    for name in ("dy", "x", "mean", "rstd", "gamma", "dsum", "dx", "dgamma", "dbeta", "stats"):
         assert bwd(L, c, **{name: P + 2}) == 1, name
     h = norm(x="bf16", w="f16", add="bf16", dy="f16", dx="bf16")
     assert fwd(L, h, x=P + 1) == 1 and fwd(L, h, gamma=P + 1) == 1 and bwd(L, h, dy=P + 1) == 1
