@@ -204,7 +204,8 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without a Stream object: 0.1 us instead of 3
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -411,7 +412,10 @@ def _torch_dtype(code: int):
 
 def _current_device() -> int:
     import torch
-    return torch.cuda.current_device() if torch.cuda.is_available() else -2   # -1 is what a CPU tensor says
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):   # no CUDA device: -1 is what a CPU tensor says, so nothing matches
+        return -2
 
 
 def _arg(fn: str, name: str, t, dev: int, dtype, n: int) -> Optional[int]:

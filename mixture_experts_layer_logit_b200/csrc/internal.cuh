@@ -217,9 +217,9 @@ cudaError_t launch_norm_bwd(const moe_norm_config& c, const void* dy, const void
                             const float* rstd, const void* gamma, const void* dsum, void* dx, float* dgamma,
                             float* dbeta, moe_stats* stats, float* part, cudaStream_t s);
 
-// Byte offsets in the balance loss's workspace: [0, part) is zeroed by the call.
+// Byte offsets in the balance loss's workspace.
 struct BalanceLayout {
-  size_t nkept, part, total;
+  size_t nkept, seq_of, part, total;
 };
 BalanceLayout balance_layout(const moe_balance_config& c);
 cudaError_t launch_balance(const moe_balance_config& c, const void* scores, const int32_t* topk, const int32_t* off,
