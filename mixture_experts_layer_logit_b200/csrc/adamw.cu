@@ -20,6 +20,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 namespace {
@@ -45,10 +46,11 @@ struct Entry {
   unsigned char pdt, gdt, bits, vec, pad[4];
 };
 constexpr int kMaxEntries = 340;
+template <int CAP>
 struct Table {
-  Entry e[kMaxEntries];
+  Entry e[CAP];
 };
-static_assert(sizeof(Table) + 128 <= 32764, "kernel parameters");
+static_assert(sizeof(Table<kMaxEntries>) + 128 <= 32764, "kernel parameters");
 
 struct Hyper {
   float lr, beta1, omb1, beta2, omb2, lnb1, lnb2, eps, one;
@@ -397,8 +399,9 @@ __device__ __forceinline__ void run_tensor(const Entry& e, long long b0, long lo
 
 // A block of threads takes a run of consecutive tiles: it looks its first
 // tensor up and walks on from there.
+template <int CAP>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
-adamw_kernel(const __grid_constant__ Table tab, int ntensors, unsigned ntiles, unsigned per_block, Hyper h,
+adamw_kernel(const __grid_constant__ Table<CAP> tab, int ntensors, unsigned ntiles, unsigned per_block, Hyper h,
              int last_launch) {
   extern __shared__ __align__(128) unsigned char staged[];
   pdl_wait();
@@ -472,8 +475,7 @@ cudaError_t launch_adamw(const moe_adamw_tensor* t, int nt, const moe_adamw_hype
   h.grad_scale = grad_scale;
   h.state = state;
   constexpr size_t kSmem = (size_t)kWarpStage * (kThreads / 32);
-  if ((err = set_smem_once<adamw_kernel>(kSmem)) != cudaSuccess) return err;
-  Table tab;
+  static thread_local Table<kMaxEntries> tab;   // 27 KB: off the caller's stack
   int i = 0;
   do {   // at least one launch: a step over nothing counts, too
     int ne = 0;
@@ -502,7 +504,16 @@ cudaError_t launch_adamw(const moe_adamw_tensor* t, int nt, const moe_adamw_hype
     }
     const unsigned most = (unsigned)di.sms * kBlocksPerSm;
     const unsigned per = std::max(1u, (tiles + most - 1) / most), blocks = std::max(1u, (tiles + per - 1) / per);
-    err = launch_pdl(adamw_kernel, dim3(blocks), dim3(kThreads), kSmem, s, tab, ne, tiles, per, h, i >= nt ? 1 : 0);
+    // the smallest parameter block that holds the tensors: a launch copies it whole
+    auto go = [&](auto cap) {
+      constexpr int CAP = decltype(cap)::value;
+      const cudaError_t set = set_smem_once<adamw_kernel<CAP>>(kSmem);
+      if (set != cudaSuccess) return set;
+      return launch_pdl(adamw_kernel<CAP>, dim3(blocks), dim3(kThreads), kSmem, s,
+                        *reinterpret_cast<const Table<CAP>*>(&tab), ne, tiles, per, h, i >= nt ? 1 : 0);
+    };
+    err = ne <= 8 ? go(std::integral_constant<int, 8>{})
+                  : ne <= 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, kMaxEntries>{});
     if (err != cudaSuccess) return err;
   } while (i < nt);
   return cudaSuccess;
