@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kBlock = MOE_ADAMW_BLOCK;
 constexpr int kThreads = 256;
-constexpr int kBlocksPerSm = 3;
+constexpr int kBlocksPerSm = 2;
 constexpr int kTile = kThreads / 32 * kBlock;   // elements a block of threads takes at a time: a block per warp
 static_assert(kBlock == 256, "a warp holds a block, eight elements a lane");
 
@@ -41,14 +41,14 @@ struct Entry {
   float* ms;
   float* vs;
   long long n;
-  float decay;        // 1 - lr wd is formed on the device (lr may be there)
-  unsigned tile0;     // first tile of the tensor
-  unsigned char pdt, gdt, bits, vec, pad[4];
+  float decay;   // 1 - lr wd is formed on the device (lr may be there)
+  unsigned char pdt, gdt, bits, vec;
 };
 constexpr int kMaxEntries = 340;
 template <int CAP>
 struct Table {
   Entry e[CAP];
+  unsigned tile0[CAP + 1];   // first tile of each tensor, then the number of tiles
 };
 static_assert(sizeof(Table<kMaxEntries>) + 128 <= 32764, "kernel parameters");
 
@@ -198,17 +198,31 @@ __device__ __forceinline__ void load_single(Raw<BITS>& r, const Entry& e, long l
   }
 }
 
-// A whole block through shared memory: the warp copies the next blocks' bytes
-// in whole lines while it works on one, and a lane reads its eight consecutive
-// elements from there.
-template <int BITS>
-struct Stage {
-  static constexpr int g = 0, p = 1024, m = 2048, v = BITS == 8 ? 2304 : 3072, bytes = BITS == 8 ? 2560 : 4096;
-  static constexpr int count = 2;
-};
-constexpr int kWarpStage = Stage<8>::bytes * Stage<8>::count > Stage<32>::bytes * Stage<32>::count
-                               ? Stage<8>::bytes * Stage<8>::count
-                               : Stage<32>::bytes * Stage<32>::count;
+// A whole block, lane l with elements 8 l .. 8 l + 7.  With 32-bit states the
+// bytes are many for the work: plain loads of 32 bytes keep the memory busy.
+__device__ __forceinline__ void load8(Raw8& r, const void* p, int dt, long long i) {
+  if (dt == MOE_DTYPE_F32)
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
+                   "=r"(r.w[7])
+                 : "l"(static_cast<const float*>(p) + i));
+  else
+    load16(static_cast<const unsigned short*>(p) + i, r.w[0], r.w[1], r.w[2], r.w[3]);
+}
+__device__ __forceinline__ void load_whole(Raw<32>& r, const Entry& e, long long b0, int lane) {
+  const long long at = b0 + lane * 8;
+  load8(r.g, e.grad, e.gdt, at);
+  if (e.master != nullptr) load8(r.p, e.master, MOE_DTYPE_F32, at);
+  else load8(r.p, e.param, e.pdt, at);
+  load8(r.m, e.m, MOE_DTYPE_F32, at);
+  load8(r.v, e.v, MOE_DTYPE_F32, at);
+}
+
+// With 8-bit states the arithmetic weighs as much as the bytes, and a block's
+// loads would have to wait for it: the warp copies its next block to shared
+// memory, in whole lines, while it works on one.
+constexpr int kStageG = 0, kStageP = 1024, kStageM = 2048, kStageV = 2304, kStageBytes = 2560;
+constexpr int kStages = 2;
 
 // 256 elements of type dt, 1024 or 512 bytes
 __device__ __forceinline__ void copy_row(uint32_t to, const void* p, int dt, long long i, int lane) {
@@ -216,18 +230,12 @@ __device__ __forceinline__ void copy_row(uint32_t to, const void* p, int dt, lon
   copy16(to + lane * 16, from);
   if (dt == MOE_DTYPE_F32) copy16(to + 512 + lane * 16, from + 512);
 }
-template <int BITS>
 __device__ __forceinline__ void copy_block(uint32_t st, const Entry& e, long long b0, int lane) {
-  copy_row(st + Stage<BITS>::g, e.grad, e.gdt, b0, lane);
-  if (e.master != nullptr) copy_row(st + Stage<BITS>::p, e.master, MOE_DTYPE_F32, b0, lane);
-  else copy_row(st + Stage<BITS>::p, e.param, e.pdt, b0, lane);
-  if constexpr (BITS == 8) {   // 16 lanes each for the codes of m and v, which lie one after the other
-    const char* from = static_cast<const char*>(lane < 16 ? e.m : e.v) + b0 + (lane & 15) * 16;
-    copy16(st + Stage<8>::m + lane * 16, from);
-  } else {
-    copy_row(st + Stage<32>::m, e.m, MOE_DTYPE_F32, b0, lane);
-    copy_row(st + Stage<32>::v, e.v, MOE_DTYPE_F32, b0, lane);
-  }
+  copy_row(st + kStageG, e.grad, e.gdt, b0, lane);
+  if (e.master != nullptr) copy_row(st + kStageP, e.master, MOE_DTYPE_F32, b0, lane);
+  else copy_row(st + kStageP, e.param, e.pdt, b0, lane);
+  // 16 lanes each for the codes of m and v, which lie one after the other
+  copy16(st + kStageM + lane * 16, static_cast<const char*>(lane < 16 ? e.m : e.v) + b0 + (lane & 15) * 16);
 }
 
 __device__ __forceinline__ void shared_row(Raw8& r, uint32_t at, int dt, int lane) {
@@ -235,17 +243,11 @@ __device__ __forceinline__ void shared_row(Raw8& r, uint32_t at, int dt, int lan
   shared16(at, r.w[0], r.w[1], r.w[2], r.w[3]);
   if (dt == MOE_DTYPE_F32) shared16(at + 16, r.w[4], r.w[5], r.w[6], r.w[7]);
 }
-template <int BITS>
-__device__ __forceinline__ void load_staged(Raw<BITS>& r, uint32_t st, const Entry& e, int lane) {
-  shared_row(r.g, st + Stage<BITS>::g, e.gdt, lane);
-  shared_row(r.p, st + Stage<BITS>::p, e.master != nullptr ? MOE_DTYPE_F32 : e.pdt, lane);
-  if constexpr (BITS == 8) {
-    shared8(st + Stage<8>::m + lane * 8, r.m.x, r.m.y);
-    shared8(st + Stage<8>::v + lane * 8, r.v.x, r.v.y);
-  } else {
-    shared_row(r.m, st + Stage<32>::m, MOE_DTYPE_F32, lane);
-    shared_row(r.v, st + Stage<32>::v, MOE_DTYPE_F32, lane);
-  }
+__device__ __forceinline__ void load_staged(Raw<8>& r, uint32_t st, const Entry& e, int lane) {
+  shared_row(r.g, st + kStageG, e.gdt, lane);
+  shared_row(r.p, st + kStageP, e.master != nullptr ? MOE_DTYPE_F32 : e.pdt, lane);
+  shared8(st + kStageM + lane * 8, r.m.x, r.m.y);
+  shared8(st + kStageV + lane * 8, r.v.x, r.v.y);
 }
 
 template <bool VEC, int BITS>
@@ -288,9 +290,14 @@ __device__ __forceinline__ void update_block(const Raw<BITS>& r, const Entry& e,
     low = min(low, min(__float_as_uint(vi.x), __float_as_uint(vi.y)));
     high = max(high, max(__float_as_uint(vi.x), __float_as_uint(vi.y)));
   }
-  if constexpr (BITS == 8) high = __reduce_max_sync(0xffffffffu, high);   // for the scale
-  const bool odd = __any_sync(0xffffffffu, low < __float_as_uint(kRootLow) || high >= 0x7f800000u);
-  if (!odd) {
+  high = __reduce_max_sync(0xffffffffu, high);
+  // all zero: an expert that has not seen a token yet.  odd: some v out of the range of root_in_range
+  const bool zero = high == 0u;
+  const bool odd = !zero && (high >= 0x7f800000u || __any_sync(0xffffffffu, low < __float_as_uint(kRootLow)));
+  if (zero) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) root[i] = 0.f;
+  } else if (!odd) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) root[i] = root_in_range(v[i]);
   } else {
@@ -332,11 +339,11 @@ __device__ __forceinline__ void update_block(const Raw<BITS>& r, const Entry& e,
     const bool inf = mt == INFINITY;
     if (inf) mt = finite_top(m);
     // the largest root is the root of the largest v
-    float vt = odd ? finite_top(root) : root_in_range(__uint_as_float(high));
+    float vt = zero ? 0.f : odd ? finite_top(root) : root_in_range(__uint_as_float(high));
     mt = fmaxf(mt, 0x1p-100f);   // the reciprocals stay finite
     vt = fmaxf(vt, 0x1p-100f);
     const uint2 cm = encode<false>(m, __fmul_rn(__frcp_rn(mt), 448.f), inf);
-    const uint2 cv = encode<true>(root, __fmul_rn(__frcp_rn(vt), 448.f), odd);
+    const uint2 cv = zero ? make_uint2(0u, 0u) : encode<true>(root, __fmul_rn(__frcp_rn(vt), 448.f), odd);
     if (lane == 0) {
       e.ms[b0 / kBlock] = __fmul_rn(mt, 1.f / 448.f);
       e.vs[b0 / kBlock] = __fmul_rn(vt, 1.f / 448.f);
@@ -353,56 +360,69 @@ __device__ __forceinline__ void update_block(const Raw<BITS>& r, const Entry& e,
   }
 }
 
-// The warp's blocks of one tensor's elements [b0, end), a tile apart.
-template <int BITS>
-__device__ __forceinline__ void run_tensor(const Entry& e, long long b0, long long end, uint32_t stages, int lane,
-                                           const Step& s) {
-  constexpr int N = Stage<BITS>::count;
+// A block whose copies are under way, and its scales.
+struct Ahead {
+  uint32_t stage;   // 0 or kStageBytes: where the next block to be worked on lies, or will
+  float ms, vs;
+};
+
+__device__ __forceinline__ bool staged8(const Entry& e, long long b0) {
+  return e.bits == 8 && e.vec && b0 + kBlock <= e.n;
+}
+__device__ __forceinline__ void start_copy(Ahead& a, const Entry& e, long long b0, uint32_t to, int lane) {
+  copy_block(to, e, b0, lane);
+  a.ms = e.ms[b0 / kBlock];
+  a.vs = e.vs[b0 / kBlock];
+}
+
+// The warp's blocks of one tensor, from b0 on, `step` apart.  8-bit states:
+// started says that the first one's copies are under way; next(to) starts those
+// of the warp's first block in the tensor that it will see next.
+template <int BITS, typename Next>
+__device__ __forceinline__ void run_tensor(const Entry e, long long b0, long long step, uint32_t stages, int lane,
+                                           const Step& s, Ahead& ahead, bool started, Next next) {
   if (e.vec) {
-    const int blocks = b0 + kBlock <= end ? (int)((end - kBlock - b0) / kTile) + 1 : 0;   // whole ones
-    float2 scale = make_float2(0.f, 0.f), ahead = scale;
-    auto scales = [&](int i) {
-      const long long k = (b0 + (long long)i * kTile) / kBlock;
-      return make_float2(e.ms[k], e.vs[k]);
-    };
-    if (BITS == 8 && blocks > 0) scale = scales(0);
-#pragma unroll
-    for (int i = 0; i < N - 1; ++i) {
-      if (i < blocks) copy_block<BITS>(stages + i * Stage<BITS>::bytes, e, b0 + (long long)i * kTile, lane);
-      copy_commit();
+    if constexpr (BITS == 8) {
+      if (!started && b0 + kBlock <= e.n) {
+        start_copy(ahead, e, b0, stages + ahead.stage, lane);
+        copy_commit();
+      }
+      while (b0 + kBlock <= e.n) {
+        Raw<8> r;
+        r.ms = ahead.ms;
+        r.vs = ahead.vs;
+        const uint32_t at = stages + ahead.stage;
+        ahead.stage ^= kStageBytes;
+        b0 += step;
+        if (b0 + kBlock <= e.n) start_copy(ahead, e, b0, stages + ahead.stage, lane);
+        else next(stages + ahead.stage);
+        copy_commit();
+        copy_wait<1>();
+        __syncwarp();   // every lane's part of the block has arrived
+        load_staged(r, at, e, lane);
+        __syncwarp();   // and has been read: the stage may be filled again
+        update_block<true, 8>(r, e, b0 - step, lane, s);
+      }
+    } else {
+      for (; b0 + kBlock <= e.n; b0 += step) {
+        Raw<32> r;
+        load_whole(r, e, b0, lane);
+        update_block<true, 32>(r, e, b0, lane, s);
+      }
     }
-    int at = 0, to = N - 1;
-    for (int i = 0; i < blocks; ++i) {
-      if (i + N - 1 < blocks)
-        copy_block<BITS>(stages + to * Stage<BITS>::bytes, e, b0 + (long long)(i + N - 1) * kTile, lane);
-      copy_commit();
-      if (BITS == 8 && i + 1 < blocks) ahead = scales(i + 1);
-      copy_wait<N - 1>();
-      __syncwarp();   // every lane's part of the block has arrived
-      Raw<BITS> r;
-      load_staged<BITS>(r, stages + at * Stage<BITS>::bytes, e, lane);
-      if constexpr (BITS == 8) r.ms = scale.x, r.vs = scale.y;
-      __syncwarp();   // and has been read: the stage may be filled again
-      update_block<true, BITS>(r, e, b0 + (long long)i * kTile, lane, s);
-      scale = ahead;
-      at = at + 1 == N ? 0 : at + 1;
-      to = to + 1 == N ? 0 : to + 1;
-    }
-    b0 += (long long)blocks * kTile;
   }
-  for (; b0 < end; b0 += kTile) {
+  for (; b0 < e.n; b0 += step) {
     Raw<BITS> r;
     load_single<BITS>(r, e, b0, lane);
     update_block<false, BITS>(r, e, b0, lane, s);
   }
 }
 
-// A block of threads takes a run of consecutive tiles: it looks its first
-// tensor up and walks on from there.
+// Tiles go round the blocks, so that all of them work on neighbouring lines and
+// a run of small tensors is shared out.
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
-adamw_kernel(const __grid_constant__ Table<CAP> tab, int ntensors, unsigned ntiles, unsigned per_block, Hyper h,
-             int last_launch) {
+adamw_kernel(const __grid_constant__ Table<CAP> tab, int ntensors, unsigned ntiles, Hyper h, int last_launch) {
   extern __shared__ __align__(128) unsigned char staged[];
   pdl_wait();
   pdl_launch_dependents();
@@ -416,25 +436,44 @@ adamw_kernel(const __grid_constant__ Table<CAP> tab, int ntensors, unsigned ntil
   // 1 - beta^t = -expm1(t ln beta): exact to rounding also for the first steps
   s.alpha = lr / expm1f(t * h.lnb1);   // -lr / c1
   s.rc2 = 1.f / sqrtf(-expm1f(t * h.lnb2));
-  const uint32_t stages = (uint32_t)__cvta_generic_to_shared(staged) + warp * kWarpStage;
-  const unsigned first = blockIdx.x * per_block, end = min(ntiles, first + per_block);
-  int lo = 0;
-  if (first < end) {
-    int hi = ntensors - 1;   // the last tensor that starts at or before the tile
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (tab.e[mid].tile0 <= first) lo = mid; else hi = mid - 1;
+  const uint32_t stages = (uint32_t)__cvta_generic_to_shared(staged) + warp * kStages * kStageBytes;
+  // the tensor of a tile, looked for from `from` on: mostly one of the next few
+  auto tensor_of = [&](unsigned tile, int from) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i, ++from)
+      if (tab.tile0[from + 1] > tile) return from;   // tile < tile0[ntensors]
+    int hi = ntensors - 1;
+    while (from < hi) {
+      const int mid = (from + hi + 1) >> 1;
+      if (tab.tile0[mid] <= tile) from = mid; else hi = mid - 1;
     }
-  }
-  for (unsigned tile = first; tile < end; ++lo) {
-    const Entry& e = tab.e[lo];
-    const unsigned stop = lo + 1 < ntensors ? min(end, tab.e[lo + 1].tile0) : end;
+    return from;
+  };
+  const long long stride = (long long)gridDim.x * kTile;
+  Ahead ahead{0, 0.f, 0.f};
+  bool started = false;
+  unsigned tile = blockIdx.x;
+  int at = tile < ntiles ? tensor_of(tile, 0) : 0;
+  while (tile < ntiles) {
+    const Entry& e = tab.e[at];
+    const unsigned stop = tab.tile0[at + 1];
+    // the block's first tile of a later tensor
+    const unsigned tile1 = tile + (stop - tile + gridDim.x - 1) / gridDim.x * gridDim.x;
+    const int at1 = tile1 < ntiles ? tensor_of(tile1, at) : at;
+    const long long b0 = (long long)(tile - tab.tile0[at]) * kTile + warp * kBlock;
+    const long long b1 = (long long)(tile1 - tab.tile0[at1]) * kTile + warp * kBlock;
+    bool started1 = false;
     s.keep = 1.f - lr * e.decay;
-    const long long b0 = (long long)(tile - e.tile0) * kTile + warp * kBlock;
-    const long long limit = min(e.n, (long long)(stop - e.tile0) * kTile);
-    if (e.bits == 8) run_tensor<8>(e, b0, limit, stages, lane, s);
-    else run_tensor<32>(e, b0, limit, stages, lane, s);
-    tile = stop;
+    auto next = [&](uint32_t to) {
+      if (tile1 >= ntiles || !staged8(tab.e[at1], b1)) return;
+      start_copy(ahead, tab.e[at1], b1, to, lane);
+      started1 = true;
+    };
+    if (e.bits == 8) run_tensor<8>(e, b0, stride, stages, lane, s, ahead, started, next);
+    else run_tensor<32>(e, b0, stride, stages, lane, s, ahead, false, next);
+    started = started1;
+    tile = tile1;
+    at = at1;
   }
   if (!last_launch) return;
   // The last block to finish counts the step: by then every block has read it.
@@ -474,8 +513,8 @@ cudaError_t launch_adamw(const moe_adamw_tensor* t, int nt, const moe_adamw_hype
   h.lr_dev = lr_dev;
   h.grad_scale = grad_scale;
   h.state = state;
-  constexpr size_t kSmem = (size_t)kWarpStage * (kThreads / 32);
-  static thread_local Table<kMaxEntries> tab;   // 27 KB: off the caller's stack
+  constexpr size_t kSmem = (size_t)kStages * kStageBytes * (kThreads / 32);
+  static thread_local Table<kMaxEntries> tab, packed;   // 28 KB each: off the caller's stack
   int i = 0;
   do {   // at least one launch: a step over nothing counts, too
     int ne = 0;
@@ -495,7 +534,7 @@ cudaError_t launch_adamw(const moe_adamw_tensor* t, int nt, const moe_adamw_hype
       e.vs = t[i].v_scale;
       e.n = t[i].n;
       e.decay = t[i].weight_decay;
-      e.tile0 = tiles;
+      tab.tile0[ne - 1] = tiles;
       e.pdt = (unsigned char)t[i].param_dtype;
       e.gdt = (unsigned char)t[i].grad_dtype;
       e.bits = (unsigned char)t[i].state_bits;
@@ -504,13 +543,16 @@ cudaError_t launch_adamw(const moe_adamw_tensor* t, int nt, const moe_adamw_hype
     }
     const unsigned most = (unsigned)di.sms * kBlocksPerSm;
     const unsigned per = std::max(1u, (tiles + most - 1) / most), blocks = std::max(1u, (tiles + per - 1) / per);
+    tab.tile0[ne] = tiles;
     // the smallest parameter block that holds the tensors: a launch copies it whole
     auto go = [&](auto cap) {
       constexpr int CAP = decltype(cap)::value;
       const cudaError_t set = set_smem_once<adamw_kernel<CAP>>(kSmem);
       if (set != cudaSuccess) return set;
-      return launch_pdl(adamw_kernel<CAP>, dim3(blocks), dim3(kThreads), kSmem, s,
-                        *reinterpret_cast<const Table<CAP>*>(&tab), ne, tiles, per, h, i >= nt ? 1 : 0);
+      Table<CAP>& t = *reinterpret_cast<Table<CAP>*>(&packed);
+      std::copy(tab.e, tab.e + ne, t.e);
+      std::copy(tab.tile0, tab.tile0 + ne + 1, t.tile0);
+      return launch_pdl(adamw_kernel<CAP>, dim3(blocks), dim3(kThreads), kSmem, s, t, ne, tiles, h, i >= nt ? 1 : 0);
     };
     err = ne <= 8 ? go(std::integral_constant<int, 8>{})
                   : ne <= 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, kMaxEntries>{});
