@@ -53,7 +53,7 @@ struct Table {
 static_assert(sizeof(Table<kMaxEntries>) + 128 <= 32764, "kernel parameters");
 
 struct Hyper {
-  float lr, beta1, omb1, beta2, omb2, lnb1, lnb2, eps, one;
+  float lr, beta1, omb1, beta2, omb2, lnb1, lnb2, eps;
   const float* lr_dev;
   const float* grad_scale;
   moe_adamw_state* state;
@@ -61,29 +61,8 @@ struct Hyper {
 
 // What every element of a step shares.
 struct Step {
-  float beta1, omb1, beta2, omb2, eps, one, gs, alpha, rc2, keep;
+  float beta1, omb1, beta2, omb2, eps, gs, alpha, rc2, keep;
 };
-
-// Two fp32 values in one instruction, each rounded on its own.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(r))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<unsigned long long&>(r))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
-        "l"(reinterpret_cast<unsigned long long&>(c)));
-  return r;
-}
-// a + b, rounded once: a product in a or b stays rounded, since `one` is not
-// known to the compiler (add.rn.f32x2 after mul.rn.f32x2 was seen to fuse)
-__device__ __forceinline__ float2 add2(float2 a, float2 b, float2 one) { return fma2(a, one, b); }
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // 1 / v to about an ulp; v is a normal number here
 __device__ __forceinline__ float reciprocal(float v) {
@@ -113,9 +92,9 @@ __device__ __forceinline__ uint2 encode(const float (&v)[8], float inv, bool odd
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float2 q = mul2(make_float2(v[2 * i], v[2 * i + 1]), both(inv));
-    if (ROOT) q = make_float2(fmaxf(q.x, 0x1p-9f), fmaxf(q.y, 0x1p-9f));
-    w[i] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+    float a = __fmul_rn(v[2 * i], inv), b = __fmul_rn(v[2 * i + 1], inv);
+    if (ROOT) a = fmaxf(a, 0x1p-9f), b = fmaxf(b, 0x1p-9f);
+    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   }
   if (odd) {
 #pragma unroll
@@ -143,9 +122,9 @@ __device__ __forceinline__ void decode(uint2 c, float scale, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w[i], __NV_E4M3);
-    const float2 f = mul2(__half22float2(*reinterpret_cast<const __half2*>(&h)), both(scale));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    v[2 * i] = __fmul_rn(f.x, scale);
+    v[2 * i + 1] = __fmul_rn(f.y, scale);
   }
 }
 
@@ -280,15 +259,12 @@ __device__ __forceinline__ void update_block(const Raw<BITS>& r, const Entry& e,
   // the bits of v >= 0 order like v, an inf's and a NaN's above all others
   unsigned low = ~0u, high = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const float2 gi = mul2(make_float2(g[i], g[i + 1]), both(s.gs));
-    const float2 mi = add2(mul2(make_float2(m[i], m[i + 1]), both(s.beta1)), mul2(gi, both(s.omb1)), both(s.one));
-    const float2 vi =
-        add2(mul2(make_float2(v[i], v[i + 1]), both(s.beta2)), mul2(mul2(gi, gi), both(s.omb2)), both(s.one));
-    m[i] = mi.x, m[i + 1] = mi.y;
-    v[i] = vi.x, v[i + 1] = vi.y;
-    low = min(low, min(__float_as_uint(vi.x), __float_as_uint(vi.y)));
-    high = max(high, max(__float_as_uint(vi.x), __float_as_uint(vi.y)));
+  for (int i = 0; i < 8; ++i) {
+    const float gi = __fmul_rn(g[i], s.gs);
+    m[i] = __fadd_rn(__fmul_rn(m[i], s.beta1), __fmul_rn(gi, s.omb1));
+    v[i] = __fadd_rn(__fmul_rn(v[i], s.beta2), __fmul_rn(__fmul_rn(gi, gi), s.omb2));
+    low = min(low, __float_as_uint(v[i]));
+    high = max(high, __float_as_uint(v[i]));
   }
   high = __reduce_max_sync(0xffffffffu, high);
   // all zero: an expert that has not seen a token yet.  odd: some v out of the range of root_in_range
@@ -305,13 +281,8 @@ __device__ __forceinline__ void update_block(const Raw<BITS>& r, const Entry& e,
     for (int i = 0; i < 8; ++i) root[i] = sqrtf(v[i]);
   }
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const float2 den = fma2(make_float2(root[i], root[i + 1]), both(s.rc2), both(s.eps));
-    const float2 upd = mul2(mul2(make_float2(m[i], m[i + 1]), both(s.alpha)),
-                            make_float2(reciprocal(den.x), reciprocal(den.y)));
-    const float2 pi = fma2(make_float2(p[i], p[i + 1]), both(s.keep), upd);
-    p[i] = pi.x, p[i + 1] = pi.y;
-  }
+  for (int i = 0; i < 8; ++i)
+    p[i] = fmaf(p[i], s.keep, m[i] * s.alpha * reciprocal(fmaf(root[i], s.rc2, s.eps)));
   if constexpr (VEC) {
     if (has_master) store8(e.master, MOE_DTYPE_F32, at, p);
     store8(e.param, e.pdt, at, p);
@@ -430,7 +401,7 @@ adamw_kernel(const __grid_constant__ Table<CAP> tab, int ntensors, unsigned ntil
   const int step = h.state->step + 1;
   const float t = (float)step;
   Step s;
-  s.beta1 = h.beta1, s.omb1 = h.omb1, s.beta2 = h.beta2, s.omb2 = h.omb2, s.eps = h.eps, s.one = h.one;
+  s.beta1 = h.beta1, s.omb1 = h.omb1, s.beta2 = h.beta2, s.omb2 = h.omb2, s.eps = h.eps;
   s.gs = h.grad_scale != nullptr ? *h.grad_scale : 1.f;
   const float lr = h.lr_dev != nullptr ? *h.lr_dev : h.lr;
   // 1 - beta^t = -expm1(t ln beta): exact to rounding also for the first steps
@@ -469,7 +440,22 @@ adamw_kernel(const __grid_constant__ Table<CAP> tab, int ntensors, unsigned ntil
       start_copy(ahead, tab.e[at1], b1, to, lane);
       started1 = true;
     };
-    if (e.bits == 8) run_tensor<8>(e, b0, stride, stages, lane, s, ahead, started, next);
+    if (e.bits == 8) {
+      // The arithmetic of 8-bit states is near the bytes' time: fp32 gradients (the layer's) of bf16 or fp16
+      // weights without a master copy get code without decisions on types (1143 us where it takes 1290).
+      Entry f = e;
+      const bool plain = e.gdt == MOE_DTYPE_F32 && e.master == nullptr;
+      if (plain) f.gdt = MOE_DTYPE_F32, f.master = nullptr;
+      if (plain && e.pdt == MOE_DTYPE_BF16) {
+        f.pdt = MOE_DTYPE_BF16;
+        run_tensor<8>(f, b0, stride, stages, lane, s, ahead, started, next);
+      } else if (plain && e.pdt == MOE_DTYPE_F16) {
+        f.pdt = MOE_DTYPE_F16;
+        run_tensor<8>(f, b0, stride, stages, lane, s, ahead, started, next);
+      } else {
+        run_tensor<8>(e, b0, stride, stages, lane, s, ahead, started, next);
+      }
+    }
     else run_tensor<32>(e, b0, stride, stages, lane, s, ahead, false, next);
     started = started1;
     tile = tile1;
@@ -509,7 +495,6 @@ cudaError_t launch_adamw(const moe_adamw_tensor* t, int nt, const moe_adamw_hype
   h.lnb1 = (float)log(hy.beta1);
   h.lnb2 = (float)log(hy.beta2);
   h.eps = (float)hy.eps;
-  h.one = 1.f;
   h.lr_dev = lr_dev;
   h.grad_scale = grad_scale;
   h.state = state;

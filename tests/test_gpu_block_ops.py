@@ -424,7 +424,7 @@ def new_state(step=0):
 SIZES = [1, 2, 7, 8, 31, 255, 256, 257, 511, 2048, 2049, 5000, 70001]
 
 
-@pytest.mark.parametrize("p,g,master", [("f32", "f32", False), ("bf16", "f32", True), ("bf16", "bf16", False),
+@pytest.mark.parametrize("p,g,master", [("f32", "f32", False), ("bf16", "f32", False), ("bf16", "f32", True), ("bf16", "bf16", False),
                                         ("f16", "f32", False), ("f16", "f16", True), ("f32", "bf16", False)])
 @pytest.mark.parametrize("bits", [8, 32])
 @pytest.mark.parametrize("off", [0, 1])
