@@ -85,6 +85,12 @@ __device__ __forceinline__ void copy_wait() {   // until at most N of the thread
 __device__ __forceinline__ void shared16(uint32_t at, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(at) : "memory");
 }
+__device__ __forceinline__ void shared4(uint32_t at, uint32_t& a) {
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void shared2(uint32_t at, uint32_t& a) {
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(a) : "r"(at) : "memory");
+}
 __device__ __forceinline__ void shared8(uint32_t at, uint32_t& a, uint32_t& b) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(at) : "memory");
 }

@@ -284,6 +284,13 @@ struct NormBwd {
   uint32_t* status;
 };
 
+// Bytes of an operand in a stage: kSingle rows may begin inside a 16-byte piece
+// and end inside another.
+template <Mode M>
+__host__ __device__ constexpr uint32_t stage_part(uint32_t bytes) {
+  return M == kSingle ? (bytes + 15u) / 16u * 16u + 16u : bytes;
+}
+
 // dx of a row at a time; the columns' sums over the block's rows stay with the
 // thread that owns the column.  The rows of the block's next rounds (one row
 // for each of its groups, which lie one after the other) come by bulk copies
@@ -297,11 +304,13 @@ __global__ void __launch_bounds__(512, NC == 1 ? 2 : 1) norm_bwd_rows_kernel(con
   __shared__ int abort_flag;
   extern __shared__ __align__(128) unsigned char dyn[];   // [stages][dy, x, dsum][groups][d]
   const Place place(a.G);
-  const int tpr = a.G.tpr, d = a.G.d, rows = a.G.rows, groups = a.G.groups, g = place.group, t = place.t;
+  const int tpr = a.G.tpr, d = a.G.d, groups = a.G.groups, g = place.group, t = place.t;
+  const unsigned rows = a.G.rows;
   const uint32_t smem = tc::smem_u32(dyn), bars = tc::smem_u32(full), done = tc::smem_u32(read);
   const uint32_t row_y = d * (a.gdt == MOE_DTYPE_F32 ? 4 : 2), row_x = d * (a.xdt == MOE_DTYPE_F32 ? 4 : 2);
   const uint32_t row_s = a.dsum == nullptr ? 0 : d * (a.odt == MOE_DTYPE_F32 ? 4 : 2);
-  const uint32_t stage = groups * (row_y + row_x + row_s);
+  const uint32_t part_y = stage_part<M>(groups * row_y), part_x = stage_part<M>(groups * row_x);
+  const uint32_t stage = part_y + part_x + (row_s == 0 ? 0 : stage_part<M>(groups * row_s));
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
       tc::mbar_init(bars + 8 * i, 1);
@@ -312,39 +321,87 @@ __global__ void __launch_bounds__(512, NC == 1 ? 2 : 1) norm_bwd_rows_kernel(con
   }
   pdl_wait();
   pdl_launch_dependents();
-  const long long step = (long long)gridDim.x * groups;
-  auto fill = [&](int to, long long r0) {   // one thread: the rows from r0 on into stage `to`
+  // rows < 2^31, and a few steps of the grid more still fit 32 bits
+  const unsigned step = gridDim.x * groups;
+  // One thread: the rows from r0 on into stage `to`.  kSingle: rows begin anywhere,
+  // and the whole 16-byte pieces that hold them are copied; the array's last
+  // bytes, where they are no whole piece, are stored one by one ahead of the
+  // arrival that makes them visible.
+  auto fill = [&](int to, unsigned r0) {
     if (r0 >= rows) return;
-    const uint32_t n = (uint32_t)min((long long)groups, rows - r0), bar = bars + 8 * to;
+    const uint32_t n = min((unsigned)groups, rows - r0), bar = bars + 8 * to;
     uint32_t at = smem + to * stage;
-    tc::mbar_expect_tx(bar, n * (row_y + row_x + row_s));
-    tc::bulk_load(at, static_cast<const char*>(a.dy) + r0 * row_y, n * row_y, bar);
-    at += groups * row_y;
-    tc::bulk_load(at, static_cast<const char*>(a.x) + r0 * row_x, n * row_x, bar);
-    at += groups * row_x;
-    if (row_s != 0) tc::bulk_load(at, static_cast<const char*>(a.dsum) + r0 * row_s, n * row_s, bar);
+    if constexpr (M != kSingle) {
+      tc::mbar_expect_tx(bar, n * (row_y + row_x + row_s));
+      tc::bulk_load(at, static_cast<const char*>(a.dy) + (size_t)r0 * row_y, n * row_y, bar);
+      at += part_y;
+      tc::bulk_load(at, static_cast<const char*>(a.x) + (size_t)r0 * row_x, n * row_x, bar);
+      at += part_x;
+      if (row_s != 0) tc::bulk_load(at, static_cast<const char*>(a.dsum) + (size_t)r0 * row_s, n * row_s, bar);
+    } else {
+      struct Piece {
+        const char* from;
+        uint32_t bytes;
+      };
+      // the whole pieces that hold the rows; what is behind the last one goes to dst at once
+      auto piece = [&](const void* p, uint32_t row_bytes, uint32_t dst) {
+        const char* base = static_cast<const char*>(p);
+        const long long total = (long long)rows * row_bytes, whole = total & ~15LL, lo = ((long long)r0 * row_bytes) & ~15LL;
+        const long long hi = min(whole, ((long long)(r0 + n) * row_bytes + 15) & ~15LL);
+        if (r0 + n == rows)
+          for (long long i = max(lo, whole); i < total; i += 2)
+            *reinterpret_cast<unsigned short*>(dyn + (dst - smem) + (i - lo)) =
+                *reinterpret_cast<const unsigned short*>(base + i);
+        return Piece{base + lo, (uint32_t)max(0LL, hi - lo)};
+      };
+      Piece q[3];
+      q[0] = piece(a.dy, row_y, at);
+      q[1] = piece(a.x, row_x, at + part_y);
+      q[2] = row_s != 0 ? piece(a.dsum, row_s, at + part_y + part_x) : Piece{nullptr, 0};
+      tc::mbar_expect_tx(bar, q[0].bytes + q[1].bytes + q[2].bytes);
+      if (q[0].bytes != 0) tc::bulk_load(at, q[0].from, q[0].bytes, bar);
+      if (q[1].bytes != 0) tc::bulk_load(at + part_y, q[1].from, q[1].bytes, bar);
+      if (q[2].bytes != 0) tc::bulk_load(at + part_y + part_x, q[2].from, q[2].bytes, bar);
+    }
   };
   __syncthreads();
-  const long long first = (long long)blockIdx.x * groups;
-  long long r0 = first;
+  unsigned r0 = blockIdx.x * groups;
   if (threadIdx.x == 0)
     for (int i = 0; i < stages; ++i) fill(i, r0 + i * step);
   // eight elements of the row that starts at `from`, chunk j
   auto fetch = [&](float (&v)[8], uint32_t from, int dt, int j) {
     Raw8 r;
-    const int c = column<M>(j, 0, t, tpr), c2 = column<M>(j, 4, t, tpr);
     if constexpr (M != kWhole) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) r.w[i] = 0u;
     }
-    if (dt == MOE_DTYPE_F32) {
-      if (inside<M>(c, d)) shared16(from + c * 4, r.w[0], r.w[1], r.w[2], r.w[3]);
-      if (inside<M>(c2, d)) shared16(from + c2 * 4, r.w[4], r.w[5], r.w[6], r.w[7]);
+    if constexpr (M == kSingle) {
+      if (dt == MOE_DTYPE_F32) {
+        from += (j * 8 * tpr + t) * 4;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (column<M>(j, i, t, tpr) < d) shared4(from + i * tpr * 4, r.w[i]);
+      } else {
+        from += (j * 8 * tpr + t) * 2;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (column<M>(j, i, t, tpr) < d) shared2(from + i * tpr * 2, r.w[i]);
+      }
     } else {
-      if (inside<M>(c, d)) shared8(from + c * 2, r.w[0], r.w[1]);
-      if (inside<M>(c2, d)) shared8(from + c2 * 2, r.w[2], r.w[3]);
+      const int c = column<M>(j, 0, t, tpr), c2 = column<M>(j, 4, t, tpr);
+      if (dt == MOE_DTYPE_F32) {
+        if (inside<M>(c, d)) shared16(from + c * 4, r.w[0], r.w[1], r.w[2], r.w[3]);
+        if (inside<M>(c2, d)) shared16(from + c2 * 4, r.w[4], r.w[5], r.w[6], r.w[7]);
+      } else {
+        if (inside<M>(c, d)) shared8(from + c * 2, r.w[0], r.w[1]);
+        if (inside<M>(c2, d)) shared8(from + c2 * 2, r.w[2], r.w[3]);
+      }
     }
-    to_float8(r, dt, v);
+    chunk_to_float<M>(r, dt, v);
+  };
+  // where the group's row begins in a part of the stage
+  auto row_at = [&](uint32_t part, uint32_t row_bytes) {
+    return part + g * row_bytes + (M == kSingle ? (r0 * row_bytes) & 15u : 0u);
   };
   float w[NC][8], dg[NC][8], db[NC][8];
 #pragma unroll
@@ -352,7 +409,7 @@ __global__ void __launch_bounds__(512, NC == 1 ? 2 : 1) norm_bwd_rows_kernel(con
     if (a.gamma != nullptr) {
       Raw8 r;
       load_chunk<M, true>(r, a.gamma, a.wdt, 0, j, t, tpr, d);
-      to_float8(r, a.wdt, w[j]);
+      chunk_to_float<M>(r, a.wdt, w[j]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -364,8 +421,9 @@ __global__ void __launch_bounds__(512, NC == 1 ? 2 : 1) norm_bwd_rows_kernel(con
   if (r0 + g < rows) mu = a.mean[r0 + g], rs = a.rstd[r0 + g];
   int turn = 0, at = 0, drains = stages;
   uint32_t phase = 0;
-  for (; r0 < rows; r0 += step, turn ^= 1) {
-    const long long row = r0 + g;
+  bool again = false;
+  for (; r0 < rows; r0 += step, turn ^= 1, again = true) {
+    const unsigned row = r0 + g;
     const bool live = row < rows;
     float mu_next = 0.f, rs_next = 0.f;
     if (row + step < rows) mu_next = a.mean[row + step], rs_next = a.rstd[row + step];
@@ -378,13 +436,13 @@ __global__ void __launch_bounds__(512, NC == 1 ? 2 : 1) norm_bwd_rows_kernel(con
       if (drains-- > 0) tc::mbar_wait(bar, parity, nullptr, tc::kDrainNs);
       return false;
     };
-    if (threadIdx.x == 0 && r0 != first) {   // the stage of the round before
+    if (threadIdx.x == 0 && again) {   // the stage of the round before
       const int to = at == 0 ? stages - 1 : at - 1;
       if (wait(done + 8 * to, at == 0 ? phase ^ 1 : phase)) fill(to, r0 + (stages - 1) * step);
     }
     wait(bars + 8 * at, phase);
-    const uint32_t from = smem + at * stage + g * row_y;
-    const uint32_t from_x = smem + at * stage + groups * row_y + g * row_x;
+    const uint32_t from = row_at(smem + at * stage, row_y);
+    const uint32_t from_x = row_at(smem + at * stage + part_y, row_x);
     float xh[NC][8], gy[NC][8];
     float2 s = make_float2(0.f, 0.f);
     if (live) {
@@ -406,7 +464,7 @@ __global__ void __launch_bounds__(512, NC == 1 ? 2 : 1) norm_bwd_rows_kernel(con
     s = row_sum(s, tpr, g, buf[turn]);
     if (live) {
       const float r1 = -rs * s.x * a.G.inv_d, r2 = -rs * s.y * a.G.inv_d;
-      const uint32_t from_s = smem + at * stage + groups * (row_y + row_x) + g * row_s;
+      const uint32_t from_s = row_at(smem + at * stage + part_y + part_x, row_s);
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
 #pragma unroll
@@ -430,7 +488,30 @@ __global__ void __launch_bounds__(512, NC == 1 ? 2 : 1) norm_bwd_rows_kernel(con
   write_columns<NC, M>(dg, db, reinterpret_cast<float*>(dyn), a.part, d, g, groups, t, tpr);
 }
 
-// The same with plain loads, for widths and pointers without vectors and for
+// Chunk j of the row at base: xh and dy; and gamma into dy.
+template <Mode M>
+__device__ __forceinline__ void read_chunk(const NormBwd& a, size_t base, float mu, float rs, int j, int t,
+                                           float (&xh)[8], float (&gy)[8]) {
+  Raw8 ry, rx;
+  load_chunk<M>(ry, a.dy, a.gdt, base, j, t, a.G.tpr, a.G.d);
+  load_chunk<M>(rx, a.x, a.xdt, base, j, t, a.G.tpr, a.G.d);
+  chunk_to_float<M>(ry, a.gdt, gy);
+  chunk_to_float<M>(rx, a.xdt, xh);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) xh[i] = (xh[i] - mu) * rs;   // of no use past the width, where dy is zero
+}
+template <Mode M>
+__device__ __forceinline__ void weigh_chunk(const NormBwd& a, int j, int t, float (&gy)[8]) {
+  if (a.gamma == nullptr) return;
+  Raw8 r;
+  float w[8];
+  load_chunk<M, true>(r, a.gamma, a.wdt, 0, j, t, a.G.tpr, a.G.d);
+  chunk_to_float<M>(r, a.wdt, w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) gy[i] *= w[i];
+}
+
+// The same with plain loads, for operands that do not begin on 16 bytes and for
 // rows too wide to keep: those (NC = 4) are read a second time, from L2.
 template <int NC, Mode M>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwd a) {
@@ -453,30 +534,11 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwd a) {
     const long long row = live ? r0 + g : 0;
     const size_t base = (size_t)row * d;
     const float mu = a.mean[row], rs = a.rstd[row];
-    // chunk j of the row: xh and dy into xh[k], gy[k]; then gamma into dy
-    auto read = [&](int j, int k) {
-      Raw8 ry, rx;
-      load_chunk<M>(ry, a.dy, a.gdt, base, j, t, tpr, d);
-      load_chunk<M>(rx, a.x, a.xdt, base, j, t, tpr, d);
-      chunk_to_float<M>(ry, a.gdt, gy[k]);
-      chunk_to_float<M>(rx, a.xdt, xh[k]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) xh[k][i] = (xh[k][i] - mu) * rs;   // of no use past the width, where dy is zero
-    };
-    auto weigh = [&](int j, int k) {
-      if (a.gamma == nullptr) return;
-      Raw8 r;
-      float w[8];
-      load_chunk<M, true>(r, a.gamma, a.wdt, 0, j, t, tpr, d);
-      chunk_to_float<M>(r, a.wdt, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) gy[k][i] *= w[i];
-    };
     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int k = KEEP ? j : 0;
-      read(j, k);
+      read_chunk<M>(a, base, mu, rs, j, t, xh[k], gy[k]);
       if (live) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -484,7 +546,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwd a) {
           db[j][i] += gy[k][i];
         }
       }
-      weigh(j, k);
+      weigh_chunk<M>(a, j, t, gy[k]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         s.x += gy[k][i];
@@ -498,8 +560,8 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwd a) {
     for (int j = 0; j < NC; ++j) {
       const int k = KEEP ? j : 0;
       if (!KEEP) {
-        read(j, k);
-        weigh(j, k);
+        read_chunk<M>(a, base, mu, rs, j, t, xh[k], gy[k]);
+        weigh_chunk<M>(a, j, t, gy[k]);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) xh[k][i] = rs * (gy[k][i] - m1 - xh[k][i] * m2);
@@ -552,8 +614,11 @@ bool vector_width(int d) { return d % 4 == 0; }
 bool on_vector(const void* p, int dt) { return reinterpret_cast<uintptr_t>(p) % (4u * dtype_bytes(dt)) == 0; }
 
 // How a row is spread over threads: tpr of them with nc chunks of eight columns
-// each.  Up to 64 chunks stay inside a warp (no barrier); above, one chunk a
-// thread as long as 512 threads reach, then two and four.
+// each.  Up to 64 chunks stay inside a warp (no barrier); above, two chunks a
+// thread (half the reductions of one: 181 against 256 us for the backward of
+// 16384 x 4096) and four where 512 threads do not reach otherwise.  A width that
+// is no multiple of four is read element by element, and one chunk leaves more
+// threads to do it (165 against 226 us for 32357 x 1037).
 struct Shape {
   int tpr, nc, threads, groups;
 };
@@ -568,7 +633,7 @@ Shape shape_of(int d) {
     s.tpr = 32;
     s.nc = 2;
   } else {
-    s.nc = chunks <= 1024 ? 2 : 4;
+    s.nc = chunks <= 512 && !vector_width(d) ? 1 : chunks <= 1024 ? 2 : 4;
     s.tpr = ((chunks + s.nc - 1) / s.nc + 31) / 32 * 32;
   }
   s.groups = std::max(1, 256 / s.tpr);
@@ -600,10 +665,9 @@ int bwd_blocks(const moe_norm_config& c, const Shape& s) {
   return (int)((rounds + per - 1) / per);
 }
 
-// Rows that bulk copies can bring: whole 16-byte pieces from 16-byte boundaries.
-bool bulk_rows(const void* p, int dt, int d) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (size_t)d * dtype_bytes(dt) % 16 == 0;
-}
+bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+// Rows that are whole 16-byte pieces from a 16-byte boundary on.
+bool whole_rows(const void* p, int dt, int d) { return on16(p) && (size_t)d * dtype_bytes(dt) % 16 == 0; }
 
 }  // namespace
 
@@ -639,30 +703,30 @@ cudaError_t launch_norm_bwd(const moe_norm_config& c, const void* dy, const void
   const size_t cols = sh.groups > 1 && weights ? (size_t)sh.groups * 2 * c.d * sizeof(float) : 0;
   const bool vec = vector_width(c.d) && on_vector(dy, c.dy_dtype) && on_vector(x, c.x_dtype) &&
                    on_vector(gamma, c.w_dtype) && on_vector(dsum, c.dx_dtype) && on_vector(dx, c.dx_dtype);
-  const bool bulk = vec && sh.nc <= 2 && bulk_rows(dy, c.dy_dtype, c.d) && bulk_rows(x, c.x_dtype, c.d) &&
-                    (dsum == nullptr || bulk_rows(dsum, c.dx_dtype, c.d));
-  // a ring of two to four rounds of rows in the block's share of an SM's shared memory
-  const size_t round = (size_t)sh.groups * c.d * (dtype_bytes(c.dy_dtype) + dtype_bytes(c.x_dtype) +
-                                                  (dsum != nullptr ? dtype_bytes(c.dx_dtype) : 0));
-  const size_t share = (size_t)(220 << 10) / bwd_resident(sh) - (2 << 10);
-  const int stages = (int)std::min<size_t>(kMaxStages, share / round);
+  const bool pieces = whole_rows(dy, c.dy_dtype, c.d) && whole_rows(x, c.x_dtype, c.d) &&
+                      (dsum == nullptr || whole_rows(dsum, c.dx_dtype, c.d));
+  const bool starts = on16(dy) && on16(x) && on16(dsum);
   const int blocks = bwd_blocks(c, sh);
+  const size_t share = (size_t)(220 << 10) / bwd_resident(sh) - (2 << 10);   // of an SM's shared memory
   const cudaError_t e = with_mode(vec, sh, c.d, [&](auto mode) {
     constexpr Mode M = decltype(mode)::value;
-    cudaError_t err;
-    if constexpr (M != kSingle) {
-      if (bulk && stages >= 2) {
-        const size_t smem = std::max(stages * round, cols);
-        auto rows = [&](auto kernel) { return launch_pdl(kernel, dim3(blocks), dim3(sh.threads), smem, s, a, stages); };
-        if (sh.nc == 1)
-          return (err = set_smem_once<norm_bwd_rows_kernel<1, M>>(220 << 10)) != cudaSuccess
-                     ? err : rows(norm_bwd_rows_kernel<1, M>);
-        return (err = set_smem_once<norm_bwd_rows_kernel<2, M>>(220 << 10)) != cudaSuccess
-                   ? err : rows(norm_bwd_rows_kernel<2, M>);
-      }
-    }
-    return launch_pdl(sh.nc == 1 ? norm_bwd_kernel<1, M> : sh.nc == 2 ? norm_bwd_kernel<2, M> : norm_bwd_kernel<4, M>,
-                      dim3(blocks), dim3(sh.threads), cols, s, a);
+    // a ring of two to four rounds of rows
+    auto part = [&](int dt) { return (size_t)stage_part<M>((uint32_t)(sh.groups * c.d * dtype_bytes(dt))); };
+    const size_t round = part(c.dy_dtype) + part(c.x_dtype) + (dsum != nullptr ? part(c.dx_dtype) : 0);
+    const int stages = (int)std::min<size_t>(kMaxStages, share / round);
+    const size_t smem = std::max(stages * round, cols);
+    auto rows = [&](auto kernel, cudaError_t set) {
+      return set != cudaSuccess ? set : launch_pdl(kernel, dim3(blocks), dim3(sh.threads), smem, s, a, stages);
+    };
+    auto plain = [&](auto kernel) { return launch_pdl(kernel, dim3(blocks), dim3(sh.threads), cols, s, a); };
+    const bool ring = M == kSingle ? starts : pieces;
+    if (sh.nc == 1)
+      return ring ? rows(norm_bwd_rows_kernel<1, M>, set_smem_once<norm_bwd_rows_kernel<1, M>>(220 << 10))
+                  : plain(norm_bwd_kernel<1, M>);
+    if (sh.nc == 2)
+      return ring ? rows(norm_bwd_rows_kernel<2, M>, set_smem_once<norm_bwd_rows_kernel<2, M>>(220 << 10))
+                  : plain(norm_bwd_kernel<2, M>);
+    return plain(norm_bwd_kernel<4, M>);
   });
   if (e != cudaSuccess || !weights) return e;
   return launch_pdl(norm_weights_kernel, dim3((2 * c.d + 31) / 32), dim3(1024), 0, s, (const float*)part, blocks,
