@@ -407,7 +407,8 @@ moe_status moe_aux_coef_next(float coef, float drop_rate, float beta, float xi, 
  * Skywork-MoE release, "训练Infra"); they give no formulas for these, and the
  * usual ones are taken.  Pointers need the alignment of their element type
  * only, workspaces 256 bytes; everything may be captured in a CUDA graph, and
- * results do not depend on the order in which blocks run.
+ * results do not depend on the order in which blocks run.  Calls that may run
+ * at the same time need workspaces of their own.
  * ---------------------------------------------------------------------------
  *
  * Layer norm over the last axis of rows x d, contiguous rows.
@@ -523,7 +524,8 @@ moe_status moe_balance_loss(const moe_balance_config* cfg, const void* scores, c
  *   p = p (1 - lr weight_decay) - lr (m / c1) / (sqrt(v / c2) + eps)
  * p is master where it is given (param is then p rounded), else param.
  *   tensors: HOST array, read during the call; every pointer in it is a device
- *     pointer.  A tensor is n >= 0 contiguous elements (0: skipped).
+ *     pointer.  A tensor is n >= 0 contiguous elements (0: skipped); no memory
+ *     that is written may appear twice.
  *     param[n] (param_dtype) and master[n] fp32 or NULL; grad[n] (grad_dtype);
  *     dtypes MOE_DTYPE_F32 | BF16 | F16.
  *     state_bits 32: m[n], v[n] fp32; m_scale, v_scale unused.

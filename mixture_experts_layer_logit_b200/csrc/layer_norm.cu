@@ -177,8 +177,8 @@ __global__ void __launch_bounds__(512, NC == 1 ? 3 : NC == 2 ? 2 : 1) norm_fwd_k
   pdl_launch_dependents();
   const Place at(a.G);
   const int tpr = a.G.tpr, d = a.G.d, t = at.t;
-  const int row = blockIdx.x * a.G.groups + at.group;
-  const bool live = row < a.G.rows;
+  const unsigned row = blockIdx.x * a.G.groups + at.group;   // up to 2^31 and a block's rows
+  const bool live = row < (unsigned)a.G.rows;
   const size_t base = (size_t)(live ? row : 0) * d;
   Raw8 rx[NC], ra[NC];
 #pragma unroll
