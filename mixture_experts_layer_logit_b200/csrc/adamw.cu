@@ -11,9 +11,14 @@
 // to zero would turn the next update into m / eps.  A value that is not finite
 // gets the NaN code and leaves its block's scale alone.
 //
-// Ten operations per element against 12 to 30 bytes: bound by those bytes.  m
-// and v are computed in separately rounded steps (no contraction), so that a
-// code does not depend on how a compiler fuses them.
+// 12 to 30 bytes an element are the floor.  32-bit states reach it (67 M
+// elements with master copies: 326 us, 6.2 TB/s); with 8-bit states some 45
+// instructions an element (two conversions each way, a root, a reciprocal, two
+// maxima) take as long as the 12 bytes, and the kernel is bound by issue as
+// much as by memory (0.55 G elements: 1175 us, 5.7 TB/s).  Hence few
+// instructions: see root_in_range, the common path of encode, and the types
+// taken out of the loop.  m and v are computed in separately rounded steps (no
+// contraction), so that a code does not depend on how a compiler fuses them.
 #include "elem8.cuh"
 
 #include <cuda_fp8.h>
@@ -27,7 +32,7 @@ namespace {
 
 constexpr int kBlock = MOE_ADAMW_BLOCK;
 constexpr int kThreads = 256;
-constexpr int kBlocksPerSm = 2;
+constexpr int kBlocksPerSm = 2;   // with three the registers spill and the memory sees more streams: 4 % slower
 constexpr int kTile = kThreads / 32 * kBlock;   // elements a block of threads takes at a time: a block per warp
 static_assert(kBlock == 256, "a warp holds a block, eight elements a lane");
 
@@ -389,8 +394,9 @@ __device__ __forceinline__ void run_tensor(const Entry e, long long b0, long lon
   }
 }
 
-// Tiles go round the blocks, so that all of them work on neighbouring lines and
-// a run of small tensors is shared out.
+// Tiles go round the blocks: all of them work on neighbouring lines (a run of
+// its own for each block took 1450 us where this took 1200), and many small
+// tensors are shared out.
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 adamw_kernel(const __grid_constant__ Table<CAP> tab, int ntensors, unsigned ntiles, Hyper h, int last_launch) {

@@ -15,7 +15,11 @@
 // read once and their gradient is written in the same pass, after a pass over
 // the indices (k of them per token) that counts.
 //
-// Bound by the bytes of the scores and their gradient.
+// The floor is the bytes of the scores and their gradient.  With few bytes per
+// score (bf16) the exponentials, the reductions over a token's lanes and the
+// bookkeeping of a token weigh as much: 16 experts to a lane spread the last two
+// (131072 x 256: 62 us with 8, 46 with 16; 56 us in fp32, where the bytes alone
+// take 43), and two blocks of 128 registers an SM beat three that spill (57 us).
 #include "elem8.cuh"
 
 #include <algorithm>
@@ -26,7 +30,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kLossBlocksPerSm = 2;   // by their registers: up to 128 with four quads a lane
+constexpr int kLossBlocksPerSm = 2;   // by their registers: up to 128 with 16 experts a lane
 constexpr int kMaxLossBlocks = 1024;
 // One block does it all up to here: 7 us for 16 x 8, 11.4 us for 256 x 64, where three kernels take 9.5 us but
 // another 5 us of launching.
@@ -170,7 +174,7 @@ struct Loss {
   double* part;
   float* loss;
   void* dscores;
-  int T, E, dt, lanes, per_warp;
+  int T, E, lanes, per_warp;
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -200,7 +204,8 @@ enum Mode { kSingle, kVector, kWhole };
 // leaves fp32's range, exp(z - max) again (sigmoid is exp there to the last
 // bit).  ex2.approx on z log2(e) adds a few units in the last place and
 // |z| / 2^24, relative.
-template <int N, Mode M, bool SIGMOID>
+// DT: the scores' type, known here so that no element asks for it.
+template <int N, Mode M, bool SIGMOID, int DT>
 __device__ __forceinline__ float loss_of_run(const Loss& a, int run, int end) {
   const int lane = threadIdx.x & 31;
   const int L = a.lanes, sub = lane & (L - 1), E = a.E, per_pass = 32 / L;
@@ -219,7 +224,7 @@ __device__ __forceinline__ float loss_of_run(const Loss& a, int run, int end) {
 #pragma unroll
     for (int q = 0; q < N; ++q) {
       if constexpr (M != kSingle) {
-        if (a.dt == MOE_DTYPE_F32) {
+        if (DT == MOE_DTYPE_F32) {
           const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(a.scores) + row + expert(q, 0));
           const uint4 v = there(q, 0) ? __ldg(p) : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
           raw[q][0] = v.x, raw[q][1] = v.y, raw[q][2] = v.z, raw[q][3] = v.w;
@@ -232,8 +237,8 @@ __device__ __forceinline__ float loss_of_run(const Loss& a, int run, int end) {
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          raw[q][i] = there(q, i) ? load_raw1(a.scores, a.dt, row + expert(q, i))
-                                  : (a.dt == MOE_DTYPE_F32 ? 0xff800000u : 0xff80u);
+          raw[q][i] = there(q, i) ? load_raw1(a.scores, DT, row + expert(q, i))
+                                  : (DT == MOE_DTYPE_F32 ? 0xff800000u : 0xff80u);
       }
     }
   };
@@ -243,11 +248,11 @@ __device__ __forceinline__ float loss_of_run(const Loss& a, int run, int end) {
 #pragma unroll
     for (int q = 0; q < N; ++q) {
       if constexpr (M != kSingle) {
-        if (there(q, 0)) store4(a.dscores, a.dt, row + expert(q, 0), d[q][0], d[q][1], d[q][2], d[q][3]);
+        if (there(q, 0)) store4(a.dscores, DT, row + expert(q, 0), d[q][0], d[q][1], d[q][2], d[q][3]);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (there(q, i)) store1(a.dscores, a.dt, row + expert(q, i), d[q][i]);
+          if (there(q, i)) store1(a.dscores, DT, row + expert(q, i), d[q][i]);
       }
     }
   };
@@ -284,10 +289,10 @@ __device__ __forceinline__ float loss_of_run(const Loss& a, int run, int end) {
       for (int q = 0; q < N; ++q)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (M != kSingle && a.dt != MOE_DTYPE_F32)
+          if (M != kSingle && DT != MOE_DTYPE_F32)
             z[q][i] = __uint_as_float(i & 1 ? raw[q][i / 2] & 0xffff0000u : raw[q][i / 2] << 16);
           else
-            z[q][i] = raw_to_float(raw[q][i], a.dt);
+            z[q][i] = raw_to_float(raw[q][i], DT);
         }
       if (next >= 0) load(t + per_pass);
       float sum = 0.f, dot = 0.f;
@@ -389,7 +394,7 @@ __device__ __forceinline__ double block_sum(double v) {
   return v;
 }
 
-template <int N, Mode M, bool SIGMOID>
+template <int N, Mode M, bool SIGMOID, int DT>
 __global__ void __launch_bounds__(kThreads, kLossBlocksPerSm) balance_loss_kernel(const Loss a) {
   __shared__ bool last;
   pdl_wait();
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, kLossBlocksPerSm) balance_loss_kerne
   // a block's warps lie far apart: padding, which costs little, is shared by all SMs
   const int run = (int)min((long long)a.T, ((long long)(threadIdx.x >> 5) * gridDim.x + blockIdx.x) * a.per_warp);
   const int end = (int)min((long long)a.T, (long long)run + a.per_warp);
-  double v = block_sum((double)loss_of_run<N, M, SIGMOID>(a, run, end));
+  double v = block_sum((double)loss_of_run<N, M, SIGMOID, DT>(a, run, end));
   if (threadIdx.x == 0) {
     a.part[blockIdx.x] = v;
     __threadfence();
@@ -416,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, kLossBlocksPerSm) balance_loss_kerne
 
 // All of it in one block, for batches so small that three launches cost more
 // than the work: the same steps with barriers between them.
-template <int N, Mode M, bool SIGMOID>
+template <int N, Mode M, bool SIGMOID, int DT>
 __global__ void __launch_bounds__(kThreads) balance_small_kernel(const Count c, const Loss a, int nhead) {
   pdl_wait();
   pdl_launch_dependents();
@@ -431,7 +436,7 @@ __global__ void __launch_bounds__(kThreads) balance_small_kernel(const Count c, 
   }
   if (a.loss == nullptr && a.dscores == nullptr) return;
   const int run = min(a.T, (int)(threadIdx.x >> 5) * a.per_warp);
-  const double v = block_sum((double)loss_of_run<N, M, SIGMOID>(a, run, min(a.T, run + a.per_warp)));
+  const double v = block_sum((double)loss_of_run<N, M, SIGMOID, DT>(a, run, min(a.T, run + a.per_warp)));
   if (threadIdx.x == 0 && a.loss != nullptr) *a.loss = (float)v;
 }
 
@@ -476,19 +481,27 @@ cudaError_t launch_balance(const moe_balance_config& c, const void* scores, cons
   const long long passes = std::max<long long>(1, ((long long)c.T + pass - 1) / pass);
   const int per_warp = (int)((passes + warps - 1) / warps) * pass;
   const Loss a{scores, seq_of,  coef, counts, nkept,   head,  reinterpret_cast<double*>(base + L.part),
-               loss,   dscores, c.T,  c.E,    c.dtype, lanes, per_warp};
-  const bool sig = c.score == MOE_SCORE_SIGMOID;
-  auto with_mode = [&](auto&& f) {
-    if (!vec) return f(std::integral_constant<Mode, kSingle>{});
-    if (c.E == 4 * lanes * n) return f(std::integral_constant<Mode, kWhole>{});
-    return f(std::integral_constant<Mode, kVector>{});
+               loss,   dscores, c.T,  c.E,    lanes, per_warp};
+  // f(mode, type, sigmoid) with the three as types
+  auto with_kind = [&](auto&& f) {
+    auto typed = [&](auto mode) {
+      using F32 = std::integral_constant<int, MOE_DTYPE_F32>;
+      using BF16 = std::integral_constant<int, MOE_DTYPE_BF16>;
+      if (c.dtype == MOE_DTYPE_F32)
+        return c.score == MOE_SCORE_SIGMOID ? f(mode, F32{}, std::true_type{}) : f(mode, F32{}, std::false_type{});
+      return c.score == MOE_SCORE_SIGMOID ? f(mode, BF16{}, std::true_type{}) : f(mode, BF16{}, std::false_type{});
+    };
+    if (!vec) return typed(std::integral_constant<Mode, kSingle>{});
+    if (c.E == 4 * lanes * n) return typed(std::integral_constant<Mode, kWhole>{});
+    return typed(std::integral_constant<Mode, kVector>{});
   };
   if (small)
-    return with_mode([&](auto mode) {
+    return with_kind([&](auto mode, auto type, auto sigmoid) {
       constexpr Mode M = decltype(mode)::value;
-      auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(1), dim3(kThreads), 0, s, count, a, nhead); };
-      if (n == 1) return sig ? go(balance_small_kernel<1, M, true>) : go(balance_small_kernel<1, M, false>);
-      return sig ? go(balance_small_kernel<2, M, true>) : go(balance_small_kernel<2, M, false>);
+      constexpr int DT = decltype(type)::value;
+      constexpr bool SIG = decltype(sigmoid)::value;
+      return launch_pdl(n == 1 ? balance_small_kernel<1, M, SIG, DT> : balance_small_kernel<2, M, SIG, DT>, dim3(1),
+                        dim3(kThreads), 0, s, count, a, nhead);
     });
   const size_t ncounts = topk != nullptr ? (size_t)c.S * c.E : 0, most = (size_t)di.sms * 4;
   const size_t words = std::max<size_t>(ncounts, nhead);
@@ -500,15 +513,14 @@ cudaError_t launch_balance(const moe_balance_config& c, const void* scores, cons
   if (loss == nullptr && dscores == nullptr) return cudaSuccess;
   const unsigned blocks =
       (unsigned)std::max<long long>(1, (((long long)c.T + per_warp - 1) / per_warp + kWarps - 1) / kWarps);
-  return with_mode([&](auto mode) {
+  return with_kind([&](auto mode, auto type, auto sigmoid) {
     constexpr Mode M = decltype(mode)::value;
-    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(blocks), dim3(kThreads), 0, s, a); };
-    switch (n) {
-      case 1: return sig ? go(balance_loss_kernel<1, M, true>) : go(balance_loss_kernel<1, M, false>);
-      case 2: return sig ? go(balance_loss_kernel<2, M, true>) : go(balance_loss_kernel<2, M, false>);
-      case 3: return sig ? go(balance_loss_kernel<3, M, true>) : go(balance_loss_kernel<3, M, false>);
-      default: return sig ? go(balance_loss_kernel<4, M, true>) : go(balance_loss_kernel<4, M, false>);
-    }
+    constexpr int DT = decltype(type)::value;
+    constexpr bool SIG = decltype(sigmoid)::value;
+    auto kernel = n == 1   ? balance_loss_kernel<1, M, SIG, DT>
+                  : n == 2 ? balance_loss_kernel<2, M, SIG, DT>
+                  : n == 3 ? balance_loss_kernel<3, M, SIG, DT> : balance_loss_kernel<4, M, SIG, DT>;
+    return launch_pdl(kernel, dim3(blocks), dim3(kThreads), 0, s, a);
   });
 }
 
