@@ -14,8 +14,8 @@
 // values (two passes over registers, not sums of squares, which cancel when
 // the mean is large).  Sums are fp32.  16384 x 4096 with an fp32 stream: forward
 // 140 us (940 MB, 6.7 TB/s), backward 172 us (1.07 GB, 6.2 TB/s).  With 16-bit
-// operands the instructions of a row (about 28 an element) take longer than its
-// bytes: 8192 x 4096 in bf16 40 us forward (3.4 TB/s).
+// operands the instructions of a row (more than 20 an element) take longer than its
+// bytes: 8192 x 4096 in bf16 36 us forward (3.7 TB/s).
 #include "elem8.cuh"
 #include "tc_ptx.cuh"
 
@@ -173,6 +173,22 @@ struct NormFwd {
   int xdt, ydt, wdt, adt;
 };
 
+// Chunk j of gamma and beta (1 and 0 without them).
+template <Mode M>
+__device__ __forceinline__ void load_affine(const NormFwd& a, int j, int t, float (&w)[8], float (&b)[8]) {
+  Raw8 r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = 1.f, b[i] = 0.f;
+  if (a.gamma != nullptr) {
+    load_chunk<M, true>(r, a.gamma, a.wdt, 0, j, t, a.G.tpr, a.G.d);
+    chunk_to_float<M>(r, a.wdt, w);
+  }
+  if (a.beta != nullptr) {
+    load_chunk<M, true>(r, a.beta, a.wdt, 0, j, t, a.G.tpr, a.G.d);
+    chunk_to_float<M>(r, a.wdt, b);
+  }
+}
+
 template <int NC, Mode M>
 __global__ void __launch_bounds__(512, NC == 1 ? 3 : NC == 2 ? 2 : 1) norm_fwd_kernel(const NormFwd a) {
   __shared__ float buf[2][kMaxWarps];
@@ -225,25 +241,78 @@ __global__ void __launch_bounds__(512, NC == 1 ? 3 : NC == 2 ? 2 : 1) norm_fwd_k
   }
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
-    Raw8 r;
     float w[8], b[8];
-    if (a.gamma != nullptr) {
-      load_chunk<M, true>(r, a.gamma, a.wdt, 0, j, t, tpr, d);
-      chunk_to_float<M>(r, a.wdt, w);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 1.f;
-    }
-    if (a.beta != nullptr) {
-      load_chunk<M, true>(r, a.beta, a.wdt, 0, j, t, tpr, d);
-      chunk_to_float<M>(r, a.wdt, b);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = 0.f;
-    }
+    load_affine<M>(a, j, t, w, b);
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[j][i] = fmaf(h[j][i] * rstd, w[i], b[i]);
     store_chunk<M>(a.y, a.ydt, base, j, t, tpr, d, h[j]);
+  }
+}
+
+// Two rows to a group of threads, without an addend: their loads, reductions and
+// barriers go together, and gamma and beta are read and converted once for both.
+template <int NC, Mode M>
+__global__ void __launch_bounds__(NC == 1 ? 512 : 256, NC == 1 ? 2 : 3) norm_fwd_pair_kernel(const NormFwd a) {
+  __shared__ float2 buf[2][kMaxWarps];
+  pdl_wait();
+  pdl_launch_dependents();
+  const Place at(a.G);
+  const int tpr = a.G.tpr, d = a.G.d, t = at.t;
+  const unsigned rows = a.G.rows, row = 2 * (blockIdx.x * a.G.groups + at.group);
+  const bool live0 = row < rows, live1 = row + 1 < rows;
+  const size_t base0 = (size_t)(live0 ? row : 0) * d, base1 = (size_t)(live1 ? row + 1 : 0) * d;
+  Raw8 r0[NC], r1[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) load_chunk<M>(r0[j], a.x, a.xdt, base0, j, t, tpr, d);
+#pragma unroll
+  for (int j = 0; j < NC; ++j) load_chunk<M>(r1[j], a.x, a.xdt, base1, j, t, tpr, d);
+  float h0[NC][8], h1[NC][8];
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    chunk_to_float<M>(r0[j], a.xdt, h0[j]);
+    chunk_to_float<M>(r1[j], a.xdt, h1[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s.x += h0[j][i];
+      s.y += h1[j][i];
+    }
+  }
+  s = row_sum(s, tpr, at.group, buf[0]);
+  const float mu0 = over(s.x, a.G.fd, a.G.inv_d), mu1 = over(s.y, a.G.fd, a.G.inv_d);
+  s = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int j = 0; j < NC; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      h0[j][i] -= mu0;
+      h1[j][i] -= mu1;
+      if (inside<M>(column<M>(j, M == kSingle ? i : i & 4, t, tpr), d)) {
+        s.x += h0[j][i] * h0[j][i];
+        s.y += h1[j][i] * h1[j][i];
+      }
+    }
+  s = row_sum(s, tpr, at.group, buf[1]);
+  const float rs0 = inverse_root(over(s.x, a.G.fd, a.G.inv_d) + a.eps);
+  const float rs1 = inverse_root(over(s.y, a.G.fd, a.G.inv_d) + a.eps);
+  if (!live0) return;
+  if (t == 0) {
+    if (a.mean != nullptr) a.mean[row] = mu0;
+    if (a.rstd != nullptr) a.rstd[row] = rs0;
+    if (a.mean != nullptr && live1) a.mean[row + 1] = mu1;
+    if (a.rstd != nullptr && live1) a.rstd[row + 1] = rs1;
+  }
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    float w[8], b[8];
+    load_affine<M>(a, j, t, w, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      h0[j][i] = fmaf(h0[j][i] * rs0, w[i], b[i]);
+      h1[j][i] = fmaf(h1[j][i] * rs1, w[i], b[i]);
+    }
+    store_chunk<M>(a.y, a.ydt, base0, j, t, tpr, d, h0[j]);
+    if (live1) store_chunk<M>(a.y, a.ydt, base1, j, t, tpr, d, h1[j]);
   }
 }
 
@@ -686,9 +755,17 @@ cudaError_t launch_norm_fwd(const moe_norm_config& c, const void* x, const void*
   const NormFwd a{geometry(c, sh), x,     add,       gamma,     beta,      y,
                   sum,             mean,  rstd,      c.eps,     c.x_dtype, c.y_dtype,
                   c.w_dtype,       c.add_dtype};
-  const dim3 grid((unsigned)(((long long)c.rows + sh.groups - 1) / sh.groups));
+  // Two rows a group without an addend, from the rows on that fill the SMs either way: 12.5 against 13.6 us for
+  // 2369 x 4096 in bf16, but 7.7 against 7.1 for 1185.  Groups of 512 threads do not have the registers.
+  const bool pair = add == nullptr && (sh.nc == 1 || (sh.nc == 2 && sh.threads <= 256)) &&
+                    c.rows >= 148LL * 12 * sh.groups;
+  const long long each = pair ? 2LL * sh.groups : sh.groups;
+  const dim3 grid((unsigned)(((long long)c.rows + each - 1) / each));
   return with_mode(vec, sh, c.d, [&](auto mode) {
     constexpr Mode M = decltype(mode)::value;
+    if (pair)
+      return launch_pdl(sh.nc == 1 ? norm_fwd_pair_kernel<1, M> : norm_fwd_pair_kernel<2, M>, grid, dim3(sh.threads), 0,
+                        s, a);
     auto kernel = sh.nc == 1 ? norm_fwd_kernel<1, M> : sh.nc == 2 ? norm_fwd_kernel<2, M> : norm_fwd_kernel<4, M>;
     return launch_pdl(kernel, grid, dim3(sh.threads), 0, s, a);
   });

@@ -94,6 +94,21 @@ def test_norm_forward(rows, d, x, y, w, at):
     within(rstd, rs, e_rs + 4 * U * rs, "rstd")
 
 
+@pytest.mark.parametrize("rows,d", [(1777, 4096), (1779, 2057), (1777, 1100), (14209, 300), (28417, 65), (113665, 24)])
+@pytest.mark.parametrize("x,y,w", [("bf16", "bf16", "bf16"), ("f32", "f16", "f32")])
+def test_norm_forward_of_many_rows(rows, d, x, y, w):
+    """Without an addend, and enough rows for two to a group of threads (an odd one is left over)."""
+    r = np.random.default_rng([rows, d, 2])
+    h = np64(dev(r.standard_normal((rows, d)) * r.uniform(0.2, 4, (rows, 1)) + r.standard_normal((rows, 1)) * 5, DT[x]))
+    G, B = dev(1 + r.standard_normal(d) * 0.3, DT[w]), dev(r.standard_normal(d), DT[w])
+    _, out, _, mean, rstd = run_norm(h, G, B, None, x, y, w)
+    ref, mu, rs = ob.layer_norm(h, np64(G), np64(B))
+    tol, e_mu, e_rs = norm_tol(h, ref, mu, rs, np64(G), np64(B), y)
+    within(out, ref, tol, "y")
+    within(mean, mu, e_mu + U * np.abs(mu), "mean")
+    within(rstd, rs, e_rs + 4 * U * rs, "rstd")
+
+
 def test_norm_without_weights_and_in_place_sum():
     r = np.random.default_rng(1)
     h, a = np64(dev(r.standard_normal((6, 640)))), dev(r.standard_normal((6, 640)))
