@@ -71,7 +71,7 @@ def norm_tol(h, y, mu, r, gamma, beta, yt):
 
 
 NORMS = [(1, 1), (1, 7), (3, 8), (2, 31), (5, 64), (9, 100), (33, 256), (17, 257), (4, 512), (2, 1000), (3, 1024),
-         (2, 2048), (300, 96), (1, 4096), (2, 4097), (7, 5120), (2, 7168), (2, 8192), (1, 11111), (2, 16384),
+         (2, 2048), (300, 96), (1, 4096), (2, 4097), (6, 4100), (7, 5120), (2, 9004), (2, 7168), (2, 8192), (1, 11111), (2, 16384),
          (1500, 520)]
 
 
@@ -214,7 +214,7 @@ def test_norm_takes_any_alignment_and_repeats_exactly(d):
     cfg = moe.make_norm_config(rows, d, x="bf16", y="f32", w="bf16", dy="bf16", dx="bf16")
     h, dy = r.standard_normal((rows, d)), r.standard_normal((rows, d))
     got = []
-    for off in (0, 0, 1, 3):
+    for off in (0, 0, 1, 3, 4):
         cut = lambda a, dt, off=off: torch.cat([torch.zeros(off, device="cuda", dtype=dt), dev(a, dt).view(-1)])[off:]  # noqa: E731, E501
         X, DY, G = cut(h, torch.bfloat16), cut(dy, torch.bfloat16), cut(np.linspace(0.5, 2, d), torch.bfloat16)
         Y, DX = cut(h * 0, torch.float32), cut(h * 0, torch.bfloat16)
@@ -286,6 +286,17 @@ def router(r, T, E, k):
 def test_balance(T, E, k, score, dt):
     r = np.random.default_rng([T, E])
     check_balance(*router(r, T, E, k), k, score=score, dt=dt)
+
+
+@pytest.mark.parametrize("T,E,k", [(80000, 16, 2), (80001, 12, 2), (80000, 10, 2), (80003, 13, 1), (40000, 24, 3),
+                                   (40000, 28, 3), (5000, 256, 8), (5001, 255, 8), (5000, 180, 4), (5003, 190, 3)])
+@pytest.mark.parametrize("score,dt", [("softmax", "f32"), ("sigmoid", "bf16"), ("sigmoid", "f32"), ("softmax", "bf16")])
+def test_balance_of_many_tokens(T, E, k, score, dt):
+    """Tokens enough for every warp: up to 16 experts to a lane, few lanes to a token."""
+    r = np.random.default_rng([T, E, 1])
+    off = np.array([0, T // 3, T // 3, T - 7, T], np.int32)
+    mask = (r.random(T) > 0.1).astype(np.uint8)
+    check_balance(*router(r, T, E, k), k, S=4, off=off, mask=mask, score=score, dt=dt)
 
 
 @pytest.mark.parametrize("T,E,k,S", [(40, 8, 2, 40), (64, 4, 1, 100), (1000, 16, 2, 7), (3000, 64, 6, 33),
@@ -470,6 +481,22 @@ def test_adamw_many_tensors_of_mixed_kinds():
         check_adam(t, s, 1, 1.0, kinds[i % 4][0])
 
 
+@pytest.mark.parametrize("p,g,master", [("bf16", "f32", False), ("f16", "f32", False), ("bf16", "bf16", True)])
+def test_adamw_several_tiles_a_block(p, g, master):
+    """Tensors of more tiles than blocks, small ones between them, both kinds of states in one plan: a block goes on
+    within a tensor and from one tensor to the next."""
+    r = np.random.default_rng(17)
+    kinds = [(1_300_000, 8, 0), (700, 8, 1), (900_123, 8, 0), (650_000, 32, 0), (256, 8, 0), (1_000_001, 8, 0), (3000, 32, 1)]
+    cases = [adam_case(r, n, p, g, bits, master, 0.1, off) for n, bits, off in kinds]
+    plan = moe.make_adamw_plan([t for t, _ in cases], lr=LR, beta1=B1, beta2=B2, eps=EPS)
+    state = new_state(2)
+    moe.moe_adamw_step(plan, state)
+    torch.cuda.synchronize()
+    assert state.tolist() == [3, 0]
+    for t, s in cases:
+        check_adam(t, s, 3, 1.0, p)
+
+
 def test_adamw_from_zero_states_over_steps_and_in_a_graph():
     """Ten steps from new states, the last seven of them replays of one captured step with the rate on the device."""
     r = np.random.default_rng(12)
@@ -585,6 +612,53 @@ def test_on_another_stream_and_in_graphs_that_share_a_workspace():
     torch.cuda.synchronize()
     for l, d, c in ((loss[0], dz[0], C[0]), (loss[1], dz[1], C[1]), (l3, d3, C3)):
         assert float(l) == want[0] and np.array_equal(np64(d), want[2]) and np.array_equal(c.cpu().numpy(), want[1])
+
+
+def test_calls_on_two_streams_at_once():
+    """The same operators on two streams, each with its own workspace, give what they give one after the other."""
+    T, E, d, n = 20000, 64, 1536, 900_000
+
+    def make(seed):
+        r = np.random.default_rng(seed)
+        z, topk = router(r, T, E, 4)
+        t, _ = adam_case(r, n, "bf16", "f32", 8, False, 0.1)
+        return dict(z=dev(z), k=dev(topk, torch.int32), x=dev(r.standard_normal((3000, d)), torch.bfloat16),
+                    dy=dev(r.standard_normal((3000, d))), t=t)
+
+    def run(a, stream):
+        out, ncfg, bcfg = {}, moe.make_norm_config(3000, d), moe.make_balance_config(T, E, 4)
+        for name, shape, dt in (("y", (3000, d), torch.bfloat16), ("dx", (3000, d), torch.bfloat16), ("mean", 3000, None),
+                                ("rstd", 3000, None), ("dg", d, None), ("db", d, None), ("loss", 1, None),
+                                ("dz", (T, E), None), ("C", (1, E), torch.int32)):
+            out[name] = torch.empty(shape, dtype=dt or torch.float32, device="cuda")
+        t = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in a["t"].items()}
+        plan, state = moe.make_adamw_plan([t], lr=LR), new_state()
+        ws1, ws2 = ws_of(moe.moe_layer_norm_workspace_size(ncfg)), ws_of(moe.moe_balance_workspace_size(bcfg))
+        torch.cuda.synchronize()
+
+        def go():
+            for _ in range(5):
+                moe.moe_layer_norm_forward(ncfg, a["x"], None, None, out["y"], mean=out["mean"], rstd=out["rstd"], stream=stream)
+                moe.moe_layer_norm_backward(ncfg, a["dy"], a["x"], out["mean"], out["rstd"], None, out["dx"], out["dg"],
+                                            out["db"], ws1, stream=stream)
+                moe.moe_balance_loss(bcfg, a["z"], a["k"], out["C"], out["loss"], ws2, dscores=out["dz"], stream=stream)
+                moe.moe_adamw_step(plan, state, stream=stream)
+        return go, {**out, **{k: v for k, v in t.items() if isinstance(v, torch.Tensor)}, "state": state}
+
+    both, streams = [make(1), make(2)], [torch.cuda.Stream() for _ in range(2)]
+    want = []
+    for a in both:
+        go, out = run(a, streams[0])
+        go()
+        torch.cuda.synchronize()
+        want.append(out)
+    got = [run(a, s) for a, s in zip(both, streams)]
+    for go, _ in got:
+        go()
+    torch.cuda.synchronize()
+    for (_, out), ref in zip(got, want):
+        for name in ref:
+            assert torch.equal(out[name].view(torch.uint8), ref[name].view(torch.uint8)), name
 
 
 def test_norm_in_a_graph():
