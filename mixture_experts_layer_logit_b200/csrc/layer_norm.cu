@@ -25,7 +25,7 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxWarps = 16;   // of a block
+constexpr int kMaxWarps = 32;   // of a block
 constexpr int kMaxStages = 4;   // of the backward's ring
 
 // How a thread sees a row.  Its columns are eight in each of its NC chunks; t of
@@ -121,7 +121,7 @@ __device__ __forceinline__ void store_chunk(void* p, int dt, size_t base, int j,
 }
 
 // Sums over the tpr threads of a row: lanes of a warp (a power of two up to 32)
-// or up to 16 whole warps (tpr a multiple of 32), whose partials meet in buf
+// or up to 32 whole warps (tpr a multiple of 32), whose partials meet in buf
 // (one entry per warp of the block) and are added by every warp for itself.
 __device__ __forceinline__ float2 add(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
 __device__ __forceinline__ float add(float a, float b) { return a + b; }
@@ -140,7 +140,12 @@ __device__ __forceinline__ T row_sum(T v, int tpr, int group, T* buf) {
     if (lane == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
     v = T{};
-    if ((lane & 15) < wpr) v = buf[group * wpr + (lane & 15)];
+    if (wpr > 16) {
+      if (lane < wpr) v = buf[lane];
+      v = add(v, from_lane(v, 16));
+    } else if ((lane & 15) < wpr) {
+      v = buf[group * wpr + (lane & 15)];
+    }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) v = add(v, from_lane(v, o));
   }
@@ -190,7 +195,7 @@ __device__ __forceinline__ void load_affine(const NormFwd& a, int j, int t, floa
 }
 
 template <int NC, Mode M>
-__global__ void __launch_bounds__(512, NC == 1 ? 3 : NC == 2 ? 2 : 1) norm_fwd_kernel(const NormFwd a) {
+__global__ void __launch_bounds__(NC == 1 ? 512 : 1024, NC == 1 ? 3 : 1) norm_fwd_kernel(const NormFwd a) {
   __shared__ float buf[2][kMaxWarps];
   pdl_wait();
   pdl_launch_dependents();
@@ -583,18 +588,25 @@ __device__ __forceinline__ void weigh_chunk(const NormBwd& a, int j, int t, floa
   for (int i = 0; i < 8; ++i) gy[i] *= w[i];
 }
 
-// The same with plain loads, for operands that do not begin on 16 bytes and for
-// rows too wide to keep: those (NC = 4) are read a second time, from L2.
+// Brings the whole 16-byte pieces of elements [base, base + d) into L2.
+__device__ __forceinline__ void prefetch_row(const void* p, int dt, size_t base, int d) {
+  const size_t es = dt == MOE_DTYPE_F32 ? 4 : 2;
+  const uintptr_t lo = (reinterpret_cast<uintptr_t>(p) + base * es + 15) & ~(uintptr_t)15;
+  const uintptr_t hi = (reinterpret_cast<uintptr_t>(p) + (base + d) * es) & ~(uintptr_t)15;
+  if (hi > lo)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(lo), "r"((uint32_t)(hi - lo)) : "memory");
+}
+
+// The same with plain loads, for operands that do not begin on 16 bytes.
 template <int NC, Mode M>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwd a) {
-  constexpr bool KEEP = NC <= 2;
   __shared__ float2 buf[2][kMaxWarps];
   extern __shared__ __align__(16) unsigned char dyn[];
   pdl_wait();
   pdl_launch_dependents();
   const Place place(a.G);
   const int tpr = a.G.tpr, d = a.G.d, rows = a.G.rows, groups = a.G.groups, g = place.group, t = place.t;
-  float dg[NC][8], db[NC][8], xh[KEEP ? NC : 1][8], gy[KEEP ? NC : 1][8];
+  float dg[NC][8], db[NC][8], xh[NC][8], gy[NC][8];
 #pragma unroll
   for (int j = 0; j < NC; ++j)
 #pragma unroll
@@ -609,20 +621,19 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwd a) {
     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const int k = KEEP ? j : 0;
-      read_chunk<M>(a, base, mu, rs, j, t, xh[k], gy[k]);
+      read_chunk<M>(a, base, mu, rs, j, t, xh[j], gy[j]);
       if (live) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          dg[j][i] += gy[k][i] * xh[k][i];
-          db[j][i] += gy[k][i];
+          dg[j][i] += gy[j][i] * xh[j][i];
+          db[j][i] += gy[j][i];
         }
       }
-      weigh_chunk<M>(a, j, t, gy[k]);
+      weigh_chunk<M>(a, j, t, gy[j]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        s.x += gy[k][i];
-        s.y += gy[k][i] * xh[k][i];
+        s.x += gy[j][i];
+        s.y += gy[j][i] * xh[j][i];
       }
     }
     s = row_sum(s, tpr, g, buf[turn]);
@@ -630,26 +641,102 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwd a) {
     if (!live) continue;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const int k = KEEP ? j : 0;
-      if (!KEEP) {
-        read_chunk<M>(a, base, mu, rs, j, t, xh[k], gy[k]);
-        weigh_chunk<M>(a, j, t, gy[k]);
-      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) xh[k][i] = rs * (gy[k][i] - m1 - xh[k][i] * m2);
+      for (int i = 0; i < 8; ++i) xh[j][i] = rs * (gy[j][i] - m1 - xh[j][i] * m2);
       if (a.dsum != nullptr) {
         Raw8 r;
         float v[8];
         load_chunk<M>(r, a.dsum, a.odt, base, j, t, tpr, d);
         chunk_to_float<M>(r, a.odt, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) xh[k][i] += v[i];
+        for (int i = 0; i < 8; ++i) xh[j][i] += v[i];
       }
-      store_chunk<M>(a.dx, a.odt, base, j, t, tpr, d, xh[k]);
+      store_chunk<M>(a.dx, a.odt, base, j, t, tpr, d, xh[j]);
     }
   }
   if (a.part == nullptr) return;
   write_columns<NC, M>(dg, db, reinterpret_cast<float*>(dyn), a.part, d, g, groups, t, tpr);
+}
+
+// Rows of more than 8192 columns, one to a block of up to 1024 threads with two
+// chunks each.  The columns' sums lie in shared memory, every thread's own as
+// float4s, which leaves the registers to the row; the next row is brought into
+// L2 meanwhile.  (Sums in the registers of 512 threads with four chunks, and the
+// row read twice: 201 us for 2048 x 16384 in fp32, and 1100 for 3727 x 9001.)
+template <Mode M>
+__global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const NormBwd a) {
+  constexpr int NC = 2;
+  __shared__ float2 buf[2][kMaxWarps];
+  extern __shared__ __align__(16) unsigned char dyn[];   // [dgamma, dbeta][2 NC][threads] of float4
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tpr = a.G.tpr, d = a.G.d, t = threadIdx.x;
+  const unsigned rows = a.G.rows;
+  float4* sums = reinterpret_cast<float4*>(dyn) + t;
+  const bool weights = a.part != nullptr;
+  if (weights) {
+#pragma unroll
+    for (int q = 0; q < 4 * NC; ++q) sums[q * tpr] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  int turn = 0;
+  for (unsigned row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
+    const size_t base = (size_t)row * d;
+    if (t == 0 && row + gridDim.x < rows) {
+      const size_t next = base + (size_t)gridDim.x * d;
+      prefetch_row(a.dy, a.gdt, next, d);
+      prefetch_row(a.x, a.xdt, next, d);
+      if (a.dsum != nullptr) prefetch_row(a.dsum, a.odt, next, d);
+    }
+    const float mu = a.mean[row], rs = a.rstd[row];
+    float xh[NC][8], gy[NC][8];
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      read_chunk<M>(a, base, mu, rs, j, t, xh[j], gy[j]);
+      if (weights) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float *x4 = xh[j] + 4 * q, *g4 = gy[j] + 4 * q;
+          float4 &dg = sums[(2 * j + q) * tpr], &db = sums[(2 * NC + 2 * j + q) * tpr];
+          const float4 og = dg, ob = db;
+          dg = make_float4(og.x + g4[0] * x4[0], og.y + g4[1] * x4[1], og.z + g4[2] * x4[2], og.w + g4[3] * x4[3]);
+          db = make_float4(ob.x + g4[0], ob.y + g4[1], ob.z + g4[2], ob.w + g4[3]);
+        }
+      }
+      weigh_chunk<M>(a, j, t, gy[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s.x += gy[j][i];
+        s.y += gy[j][i] * xh[j][i];
+      }
+    }
+    s = row_sum(s, tpr, 0, buf[turn]);
+    const float r1 = -rs * s.x * a.G.inv_d, r2 = -rs * s.y * a.G.inv_d;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xh[j][i] = fmaf(xh[j][i], r2, fmaf(gy[j][i], rs, r1));
+      if (a.dsum != nullptr) {
+        Raw8 r;
+        float v[8];
+        load_chunk<M>(r, a.dsum, a.odt, base, j, t, tpr, d);
+        chunk_to_float<M>(r, a.odt, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xh[j][i] += v[i];
+      }
+      store_chunk<M>(a.dx, a.odt, base, j, t, tpr, d, xh[j]);
+    }
+  }
+  if (!weights) return;
+  float dg[NC][8], db[NC][8];
+#pragma unroll
+  for (int j = 0; j < NC; ++j)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      *reinterpret_cast<float4*>(&dg[j][4 * q]) = sums[(2 * j + q) * tpr];
+      *reinterpret_cast<float4*>(&db[j][4 * q]) = sums[(2 * NC + 2 * j + q) * tpr];
+    }
+  write_columns<NC, M>(dg, db, nullptr, a.part, d, 0, 1, t, tpr);
 }
 
 // dgamma and dbeta: the blocks' partial sums of each column.  A block takes 32
@@ -688,9 +775,9 @@ bool on_vector(const void* p, int dt) { return reinterpret_cast<uintptr_t>(p) % 
 // How a row is spread over threads: tpr of them with nc chunks of eight columns
 // each.  Up to 64 chunks stay inside a warp (no barrier); above, two chunks a
 // thread (half the reductions of one: 181 against 256 us for the backward of
-// 16384 x 4096) and four where 512 threads do not reach otherwise.  A width that
-// is no multiple of four is read element by element, and one chunk leaves more
-// threads to do it (165 against 226 us for 32357 x 1037).
+// 16384 x 4096), up to 1024 threads.  A width that is no multiple of four is read
+// element by element, and one chunk leaves more threads to do it (165 against
+// 226 us for 32357 x 1037).
 struct Shape {
   int tpr, nc, threads, groups;
 };
@@ -705,13 +792,15 @@ Shape shape_of(int d) {
     s.tpr = 32;
     s.nc = 2;
   } else {
-    s.nc = chunks <= 512 && !vector_width(d) ? 1 : chunks <= 1024 ? 2 : 4;
+    s.nc = chunks <= 512 && !vector_width(d) ? 1 : 2;
     s.tpr = ((chunks + s.nc - 1) / s.nc + 31) / 32 * 32;
   }
   s.groups = std::max(1, 256 / s.tpr);
   s.threads = s.groups * s.tpr;
   return s;
 }
+
+constexpr int kWide = 8192;   // columns of 512 threads with two chunks
 
 Geometry geometry(const moe_norm_config& c, const Shape& s) {
   return Geometry{c.rows,   c.d, s.tpr, s.groups, (unsigned)((65536 + s.tpr - 1) / s.tpr),
@@ -766,8 +855,7 @@ cudaError_t launch_norm_fwd(const moe_norm_config& c, const void* x, const void*
     if (pair)
       return launch_pdl(sh.nc == 1 ? norm_fwd_pair_kernel<1, M> : norm_fwd_pair_kernel<2, M>, grid, dim3(sh.threads), 0,
                         s, a);
-    auto kernel = sh.nc == 1 ? norm_fwd_kernel<1, M> : sh.nc == 2 ? norm_fwd_kernel<2, M> : norm_fwd_kernel<4, M>;
-    return launch_pdl(kernel, grid, dim3(sh.threads), 0, s, a);
+    return launch_pdl(sh.nc == 1 ? norm_fwd_kernel<1, M> : norm_fwd_kernel<2, M>, grid, dim3(sh.threads), 0, s, a);
   });
 }
 
@@ -793,20 +881,23 @@ cudaError_t launch_norm_bwd(const moe_norm_config& c, const void* dy, const void
     // a ring of two to four rounds of rows
     auto part = [&](int dt) { return (size_t)stage_part<M>((uint32_t)(sh.groups * c.d * dtype_bytes(dt))); };
     const size_t round = part(c.dy_dtype) + part(c.x_dtype) + (dsum != nullptr ? part(c.dx_dtype) : 0);
-    const int stages = (int)std::min<size_t>(kMaxStages, share / round);
+    const int stages = (int)std::min<size_t>(kMaxStages, std::max<size_t>(1, share / round));
     const size_t smem = std::max(stages * round, cols);
     auto rows = [&](auto kernel, cudaError_t set) {
       return set != cudaSuccess ? set : launch_pdl(kernel, dim3(blocks), dim3(sh.threads), smem, s, a, stages);
     };
     auto plain = [&](auto kernel) { return launch_pdl(kernel, dim3(blocks), dim3(sh.threads), cols, s, a); };
     const bool ring = M == kSingle ? starts : pieces;
+    if (c.d > kWide) {
+      const size_t sums = weights ? (size_t)sh.threads * 8 * sizeof(float4) : 0;
+      const cudaError_t set = set_smem_once<norm_bwd_wide_kernel<M>>(1024 * 8 * sizeof(float4));
+      return set != cudaSuccess ? set : launch_pdl(norm_bwd_wide_kernel<M>, dim3(blocks), dim3(sh.threads), sums, s, a);
+    }
     if (sh.nc == 1)
       return ring ? rows(norm_bwd_rows_kernel<1, M>, set_smem_once<norm_bwd_rows_kernel<1, M>>(220 << 10))
                   : plain(norm_bwd_kernel<1, M>);
-    if (sh.nc == 2)
-      return ring ? rows(norm_bwd_rows_kernel<2, M>, set_smem_once<norm_bwd_rows_kernel<2, M>>(220 << 10))
-                  : plain(norm_bwd_kernel<2, M>);
-    return plain(norm_bwd_kernel<4, M>);
+    return ring ? rows(norm_bwd_rows_kernel<2, M>, set_smem_once<norm_bwd_rows_kernel<2, M>>(220 << 10))
+                : plain(norm_bwd_kernel<2, M>);
   });
   if (e != cudaSuccess || !weights) return e;
   return launch_pdl(norm_weights_kernel, dim3((2 * c.d + 31) / 32), dim3(1024), 0, s, (const float*)part, blocks,
