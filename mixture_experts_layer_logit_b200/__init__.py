@@ -482,8 +482,8 @@ def moe_layer_norm_backward(cfg, dy, x, mean, rstd, gamma, dx, dgamma=None, dbet
         _arg(fn, "x", x, dev, _torch_dtype(cfg.x_dtype), n), _arg(fn, "mean", mean, dev, f32, cfg.rows),
         _arg(fn, "rstd", rstd, dev, f32, cfg.rows), _arg(fn, "gamma", gamma, dev, _torch_dtype(cfg.w_dtype), cfg.d),
         _arg(fn, "dsum", dsum, dev, dxt, n), _arg(fn, "dx", dx, dev, dxt, n),
-        _arg(fn, "dgamma", dgamma, dev, f32, cfg.d), _arg(fn, "dbeta", dbeta, dev, f32, cfg.d), _stats(fn, stats, dev), wp, wn,
-        _stream(stream)))
+        _arg(fn, "dgamma", dgamma, dev, f32, cfg.d), _arg(fn, "dbeta", dbeta, dev, f32, cfg.d),
+        _stats(fn, stats, dev), wp, wn, _stream(stream)))
 
 
 def moe_route_scores(cfg, x, Wg, bg, topk_idx, topk_w, gap, prob_mean, scores, ws, stream=None, z_loss=None):

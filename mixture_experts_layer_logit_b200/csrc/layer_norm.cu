@@ -423,7 +423,8 @@ __global__ void __launch_bounds__(512, NC == 1 ? 2 : 1) norm_bwd_rows_kernel(con
       // the whole pieces that hold the rows; what is behind the last one goes to dst at once
       auto piece = [&](const void* p, uint32_t row_bytes, uint32_t dst) {
         const char* base = static_cast<const char*>(p);
-        const long long total = (long long)rows * row_bytes, whole = total & ~15LL, lo = ((long long)r0 * row_bytes) & ~15LL;
+        const long long total = (long long)rows * row_bytes, whole = total & ~15LL;
+        const long long lo = ((long long)r0 * row_bytes) & ~15LL;
         const long long hi = min(whole, ((long long)(r0 + n) * row_bytes + 15) & ~15LL);
         if (r0 + n == rows)
           for (long long i = max(lo, whole); i < total; i += 2)
