@@ -662,8 +662,11 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwd a) {
 // Rows of more than 8192 columns, one to a block of up to 1024 threads with two
 // chunks each.  The columns' sums lie in shared memory, every thread's own as
 // float4s, which leaves the registers to the row; the next row is brought into
-// L2 meanwhile.  (Sums in the registers of 512 threads with four chunks, and the
-// row read twice: 201 us for 2048 x 16384 in fp32, and 1100 for 3727 x 9001.)
+// L2 meanwhile (125 us without that).  2048 x 16384 in fp32: 118 us, 4.6 TB/s;
+// 3727 x 9001: 219.  With one block an SM most of the waiting is for the row's
+// loads (8.7 of some 22 cycles an issue; shared memory 3.2, the barrier 1.5).
+// Sums in the registers of 512 threads with four chunks, and the row read
+// twice, took 201 and 1100 us.
 template <Mode M>
 __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const NormBwd a) {
   constexpr int NC = 2;
