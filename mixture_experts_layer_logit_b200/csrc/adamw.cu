@@ -19,6 +19,7 @@
 // instructions: see root_in_range, the common path of encode, and the types
 // taken out of the loop.  m and v are computed in separately rounded steps (no
 // contraction), so that a code does not depend on how a compiler fuses them.
+#include "adamw_access.cuh"
 #include "elem8.cuh"
 
 #include <cuda_fp8.h>
@@ -476,15 +477,6 @@ adamw_kernel(const __grid_constant__ Table<CAP> tab, int ntensors, unsigned ntil
   }
 }
 
-// Every array of the tensor allows 16-byte copies and, where it is written, a
-// lane's store of eight elements at once.
-bool vector_aligned(const moe_adamw_tensor& t) {
-  auto on = [](const void* p, unsigned bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
-  const unsigned st = t.state_bits == 8 ? 16u : 32u;
-  return on(t.param, 8u * dtype_bytes(t.param_dtype)) && on(t.grad, 16u) && on(t.master, 32u) && on(t.m, st) &&
-         on(t.v, st);
-}
-
 }  // namespace
 
 cudaError_t launch_adamw(const moe_adamw_tensor* t, int nt, const moe_adamw_hyper& hy, const float* lr_dev,
@@ -529,7 +521,7 @@ cudaError_t launch_adamw(const moe_adamw_tensor* t, int nt, const moe_adamw_hype
       e.pdt = (unsigned char)t[i].param_dtype;
       e.gdt = (unsigned char)t[i].grad_dtype;
       e.bits = (unsigned char)t[i].state_bits;
-      e.vec = vector_aligned(t[i]) ? 1 : 0;
+      e.vec = adamw_by_vectors(t[i]) ? 1 : 0;
       tiles += (unsigned)nt_i;
     }
     const unsigned most = (unsigned)di.sms * kBlocksPerSm;
