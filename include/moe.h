@@ -423,6 +423,10 @@ moe_status moe_aux_coef_next(float coef, float drop_rate, float beta, float xi, 
  *   add[rows, d] or NULL; sum[rows, d] or NULL receives h (only with add; it
  *   may be x itself); gamma[d], beta[d] or NULL (1, 0); mean[rows], rstd[rows]
  *   fp32 or NULL receive mu and 1 / sqrt(var + eps).
+ *   Sums that leave fp32's range are infinite: a row with an infinite element
+ *   has that mean and NaN for rstd and y (all NaN with infinities of both signs
+ *   or a NaN); a finite row with squared deviations past the range (above some
+ *   1e19) has rstd 0 and y = beta.  Other rows do not notice.
  * moe_layer_norm_backward: the gradients of <dy, y> + <dsum, h> with respect
  *   to h (which are those of x and of add), gamma and beta.
  *   dy[rows, d]; x[rows, d]: h of the forward (its sum when add was given);

@@ -152,16 +152,20 @@ __device__ __forceinline__ T row_sum(T v, int tpr, int group, T* buf) {
   return v;
 }
 
-// s / d rounded to nearest, with inv = 1 / d: the quotient's exact residual corrects it
+// s / d rounded to nearest, with inv = 1 / d: the quotient's exact residual
+// corrects it (Markstein's correction step).  An infinite s has no residual and
+// stays infinite.
 __device__ __forceinline__ float over(float s, float d, float inv) {
   const float q = s * inv;
-  return fmaf(fmaf(-q, d, s), inv, q);
+  return isinf(q) ? q : fmaf(fmaf(-q, d, s), inv, q);
 }
 
-// 1 / sqrt(v) to about an ulp: one Newton step on the approximation
+// 1 / sqrt(v) to about an ulp: one Newton step on the approximation (which is
+// 0 for an infinite v, and stays so).  The half goes with y, of which it is
+// exact: v may be subnormal.
 __device__ __forceinline__ float inverse_root(float v) {
   const float y = rsqrtf(v);
-  return y * fmaf(-0.5f * v * y, y, 1.5f);
+  return v == INFINITY ? y : y * fmaf(-0.5f * y * v, y, 1.5f);
 }
 
 struct NormFwd {
