@@ -435,7 +435,8 @@ moe_status moe_aux_coef_next(float coef, float drop_rate, float beta, float xi, 
  *   dy when dy_dtype is dx_dtype); dgamma[d], dbeta[d] fp32 or NULL, fully written
  *   (zeros when rows is 0), summed in a fixed order.
  *   stats: device moe_stats or NULL; a bounded wait that gave up sets
- *   MOE_DEV_TIMEOUT in status.
+ *   MOE_DEV_TIMEOUT in status.  With or without stats, dx of the rows that it
+ *   missed, dgamma and dbeta are NaN then.
  *   ws: moe_layer_norm_workspace_size(cfg) bytes; not read when dgamma and
  *   dbeta are both NULL.
  */
@@ -590,6 +591,17 @@ moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t ntensors, con
  * outside tests.
  */
 moe_status moe_testing_set_expert_wait(uint64_t wait_ns, int32_t extra_dependency);
+
+/*
+ * The same for moe_layer_norm_backward, whose blocks wait for copies of their
+ * rows (operands on 16 bytes, widths up to 8192 whose rows are whole 16-byte
+ * pieces or no multiple of four elements):
+ *   wait_ns: limit of the waits, as above;
+ *   kept_rounds: each block copies its first kept_rounds rounds of rows and no
+ *     more, so that its waits for later ones run out (-1 = all of them).
+ * MOE_ERR_ARG for wait_ns > 60 s or kept_rounds < -1.
+ */
+moe_status moe_testing_set_norm_wait(uint64_t wait_ns, int32_t kept_rounds);
 
 /* Size of the library's fixed device scratch array used by moe_permute_static. */
 #define MOE_STATIC_SCRATCH_BYTES (2u << 20)

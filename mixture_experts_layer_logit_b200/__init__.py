@@ -25,7 +25,8 @@ __all__ = [
     "moe_status_string", "moe_scratch_size", "moe_workspace_size", "moe_route", "moe_permute",
     "moe_expert_ffn", "moe_combine", "moe_layer_forward", "moe_convert_bf16_to_f16", "moe_permute_static",
     "moe_expert_ffn_combine", "MOE_STATIC_SCRATCH_BYTES", "prepare_w2", "moe_aux_coef_update",
-    "moe_aux_coef_next", "moe_testing_set_expert_wait", "moe_segments_scratch_size", "moe_expert_ffn_segments",
+    "moe_aux_coef_next", "moe_testing_set_expert_wait", "moe_testing_set_norm_wait", "moe_segments_scratch_size",
+    "moe_expert_ffn_segments",
     "moe_backward_workspace_size", "moe_layer_backward", "moe_mxfp8_weight_bytes", "moe_prepare_mxfp8_weights",
     "moe_workspace_size_mxfp8", "moe_layer_forward_mxfp8", "prepare_mxfp8", "moe_workspace_size_shared",
     "moe_layer_forward_shared",
@@ -49,6 +50,7 @@ EXPORTED_SYMBOLS = ["moe_status_string", "moe_scratch_size", "moe_workspace_size
                     "moe_permute", "moe_expert_ffn", "moe_combine", "moe_layer_forward",
                     "moe_convert_bf16_to_f16", "moe_permute_static", "moe_expert_ffn_combine",
                     "moe_aux_coef_update", "moe_aux_coef_next", "moe_testing_set_expert_wait",
+                    "moe_testing_set_norm_wait",
                     "moe_segments_scratch_size", "moe_expert_ffn_segments", "moe_backward_workspace_size",
                     "moe_layer_backward", "moe_mxfp8_weight_bytes", "moe_prepare_mxfp8_weights",
                     "moe_workspace_size_mxfp8", "moe_layer_forward_mxfp8", "moe_workspace_size_shared",
@@ -137,6 +139,7 @@ def lib() -> ctypes.CDLL:
     L.moe_aux_coef_update.argtypes = [P, P, f32, f32, P]
     L.moe_aux_coef_next.argtypes = [f32, f32, f32, f32, ctypes.POINTER(f32)]
     L.moe_testing_set_expert_wait.argtypes = [ctypes.c_uint64, ctypes.c_int32]
+    L.moe_testing_set_norm_wait.argtypes = [ctypes.c_uint64, ctypes.c_int32]
     i32 = ctypes.c_int32
     L.moe_segments_scratch_size.argtypes = [cfgp, i32, i32]
     L.moe_segments_scratch_size.restype = ctypes.c_size_t
@@ -170,7 +173,8 @@ def lib() -> ctypes.CDLL:
     L.moe_adamw_step.argtypes = [ctypes.POINTER(moe_adamw_tensor), i32, ctypes.POINTER(moe_adamw_hyper), P, P, P, P]
     for n in ["moe_route", "moe_permute", "moe_expert_ffn", "moe_combine", "moe_layer_forward",
               "moe_convert_bf16_to_f16", "moe_permute_static", "moe_expert_ffn_combine", "moe_aux_coef_update",
-              "moe_aux_coef_next", "moe_testing_set_expert_wait", "moe_expert_ffn_segments", "moe_layer_backward",
+              "moe_aux_coef_next", "moe_testing_set_expert_wait", "moe_testing_set_norm_wait",
+              "moe_expert_ffn_segments", "moe_layer_backward",
               "moe_prepare_mxfp8_weights", "moe_layer_forward_mxfp8", "moe_layer_forward_shared",
               "moe_layer_norm_forward", "moe_layer_norm_backward", "moe_route_scores", "moe_layer_forward_scores",
               "moe_layer_backward_scores", "moe_balance_loss", "moe_adamw_step"]:
@@ -316,6 +320,12 @@ def moe_testing_set_expert_wait(wait_ns: int, extra_dependency: int):
     """Test hook: limit of the one-launch expert kernel's waits (0 = default)
     and an amount added to its layer-2 dependency target (> 0: unreachable)."""
     _check("moe_testing_set_expert_wait", lib().moe_testing_set_expert_wait(wait_ns, extra_dependency))
+
+
+def moe_testing_set_norm_wait(wait_ns: int, kept_rounds: int):
+    """Test hook: limit of the norm backward's waits (0 = default) and how many
+    rounds of rows each of its blocks copies (-1: all)."""
+    _check("moe_testing_set_norm_wait", lib().moe_testing_set_norm_wait(wait_ns, kept_rounds))
 
 
 def moe_workspace_size_shared(cfg: moe_config, F_shared: int) -> int:

@@ -961,4 +961,10 @@ moe_status moe_testing_set_expert_wait(uint64_t wait_ns, int32_t extra_dependenc
   return MOE_OK;
 }
 
+moe_status moe_testing_set_norm_wait(uint64_t wait_ns, int32_t kept_rounds) {
+  if (wait_ns > 60000000000ull || kept_rounds < -1) return MOE_ERR_ARG;
+  set_norm_test_hooks(wait_ns, kept_rounds);
+  return MOE_OK;
+}
+
 }  // extern "C"

@@ -216,6 +216,8 @@ cudaError_t launch_norm_fwd(const moe_norm_config& c, const void* x, const void*
 cudaError_t launch_norm_bwd(const moe_norm_config& c, const void* dy, const void* x, const float* mean,
                             const float* rstd, const void* gamma, const void* dsum, void* dx, float* dgamma,
                             float* dbeta, moe_stats* stats, float* part, cudaStream_t s);
+// Test hooks of its bounded waits (see moe_testing_set_norm_wait).
+void set_norm_test_hooks(unsigned long long wait_ns, int kept_rounds);
 
 // Byte offsets in the balance loss's workspace.
 struct BalanceLayout {

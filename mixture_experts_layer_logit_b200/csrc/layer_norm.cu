@@ -20,6 +20,7 @@
 #include "tc_ptx.cuh"
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 namespace moe {
@@ -379,7 +380,8 @@ __host__ __device__ constexpr uint32_t stage_part(uint32_t bytes) {
 // threads spend nothing on loads, and a stage is filled again as soon as every
 // warp has read it.
 template <int NC, Mode M>
-__global__ void __launch_bounds__(512, NC == 1 ? 2 : 1) norm_bwd_rows_kernel(const NormBwd a, int stages) {
+__global__ void __launch_bounds__(512, NC == 1 ? 2 : 1)
+norm_bwd_rows_kernel(const NormBwd a, int stages, unsigned copied, unsigned long long wait_ns) {
   __shared__ float2 buf[2][kMaxWarps];
   __shared__ unsigned long long full[kMaxStages], read[kMaxStages];
   __shared__ int abort_flag;
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(512, NC == 1 ? 2 : 1) norm_bwd_rows_kernel(con
   // bytes, where they are no whole piece, are stored one by one ahead of the
   // arrival that makes them visible.
   auto fill = [&](int to, unsigned r0) {
-    if (r0 >= rows) return;
+    if (r0 >= copied) return;
     const uint32_t n = min((unsigned)groups, rows - r0), bar = bars + 8 * to;
     uint32_t at = smem + to * stage;
     if constexpr (M != kSingle) {
@@ -509,10 +511,11 @@ __global__ void __launch_bounds__(512, NC == 1 ? 2 : 1) norm_bwd_rows_kernel(con
     const bool live = row < rows;
     float mu_next = 0.f, rs_next = 0.f;
     if (row + step < rows) mu_next = a.mean[row + step], rs_next = a.rstd[row + step];
-    // a wait that runs out: the status says so, no more copies are issued, and
-    // those under way are given a little longer
+    // a wait that runs out: the status says so, no more copies are issued, those
+    // under way are given a little longer, and the thread's share of this row and
+    // all later ones (whose phases mean nothing any more) is NaN
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (tc::mbar_try_wait(bar, parity) || tc::mbar_wait(bar, parity, &abort_flag, tc::kWaitNs)) return true;
+      if (tc::mbar_try_wait(bar, parity) || tc::mbar_wait(bar, parity, &abort_flag, wait_ns)) return true;
       abort_flag = 1;
       if (a.status != nullptr) atomicOr(a.status, MOE_DEV_TIMEOUT);
       if (drains-- > 0) tc::mbar_wait(bar, parity, nullptr, tc::kDrainNs);
@@ -523,6 +526,7 @@ __global__ void __launch_bounds__(512, NC == 1 ? 2 : 1) norm_bwd_rows_kernel(con
       if (wait(done + 8 * to, at == 0 ? phase ^ 1 : phase)) fill(to, r0 + (stages - 1) * step);
     }
     wait(bars + 8 * at, phase);
+    if (drains != stages) mu = NAN;   // takes xh with it, and so dgamma and the row's sums
     const uint32_t from = row_at(smem + at * stage, row_y);
     const uint32_t from_x = row_at(smem + at * stage + part_y, row_x);
     float xh[NC][8], gy[NC][8];
@@ -566,6 +570,12 @@ __global__ void __launch_bounds__(512, NC == 1 ? 2 : 1) norm_bwd_rows_kernel(con
     if (++at == stages) at = 0, phase ^= 1;
   }
   if (a.part == nullptr) return;
+  if (drains != stages) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) db[j][i] = NAN;
+  }
   __syncthreads();   // the stages are free: the columns of the block's rows meet there
   write_columns<NC, M>(dg, db, reinterpret_cast<float*>(dyn), a.part, d, g, groups, t, tpr);
 }
@@ -838,7 +848,15 @@ bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 // Rows that are whole 16-byte pieces from a 16-byte boundary on.
 bool whole_rows(const void* p, int dt, int d) { return on16(p) && (size_t)d * dtype_bytes(dt) % 16 == 0; }
 
+std::atomic<unsigned long long> g_wait_ns{tc::kWaitNs};
+std::atomic<int> g_kept_rounds{-1};
+
 }  // namespace
+
+void set_norm_test_hooks(unsigned long long wait_ns, int kept_rounds) {
+  g_wait_ns.store(wait_ns != 0 ? wait_ns : tc::kWaitNs, std::memory_order_relaxed);
+  g_kept_rounds.store(kept_rounds, std::memory_order_relaxed);
+}
 
 // Each block leaves one partial of the weights' gradient.
 int norm_bwd_blocks(const moe_norm_config& c) { return bwd_blocks(c, shape_of(c.d)); }
@@ -872,6 +890,11 @@ cudaError_t launch_norm_bwd(const moe_norm_config& c, const void* dy, const void
                             float* dbeta, moe_stats* stats, float* part, cudaStream_t s) {
   const Shape sh = shape_of(c.d);
   const bool weights = dgamma != nullptr || dbeta != nullptr;
+  const int blocks = bwd_blocks(c, sh);
+  const int kept = g_kept_rounds.load(std::memory_order_relaxed);
+  const unsigned long long wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+  const unsigned copied =   // rows before this one are copied: all of them, but in a test
+      (unsigned)(kept < 0 ? c.rows : std::min<long long>(c.rows, (long long)kept * blocks * sh.groups));
   const NormBwd a{geometry(c, sh),          dy,        x,         mean,       rstd,       gamma, dsum, dx,
                   weights ? part : nullptr, c.x_dtype, c.w_dtype, c.dy_dtype, c.dx_dtype,
                   stats != nullptr ? &stats->status : nullptr};
@@ -882,7 +905,6 @@ cudaError_t launch_norm_bwd(const moe_norm_config& c, const void* dy, const void
   const bool pieces = whole_rows(dy, c.dy_dtype, c.d) && whole_rows(x, c.x_dtype, c.d) &&
                       (dsum == nullptr || whole_rows(dsum, c.dx_dtype, c.d));
   const bool starts = on16(dy) && on16(x) && on16(dsum);
-  const int blocks = bwd_blocks(c, sh);
   const size_t share = (size_t)(220 << 10) / bwd_resident(sh) - (2 << 10);   // of an SM's shared memory
   const cudaError_t e = with_mode(vec, sh, c.d, [&](auto mode) {
     constexpr Mode M = decltype(mode)::value;
@@ -892,7 +914,8 @@ cudaError_t launch_norm_bwd(const moe_norm_config& c, const void* dy, const void
     const int stages = (int)std::min<size_t>(kMaxStages, std::max<size_t>(1, share / round));
     const size_t smem = std::max(stages * round, cols);
     auto rows = [&](auto kernel, cudaError_t set) {
-      return set != cudaSuccess ? set : launch_pdl(kernel, dim3(blocks), dim3(sh.threads), smem, s, a, stages);
+      return set != cudaSuccess ? set
+                                : launch_pdl(kernel, dim3(blocks), dim3(sh.threads), smem, s, a, stages, copied, wait_ns);
     };
     auto plain = [&](auto kernel) { return launch_pdl(kernel, dim3(blocks), dim3(sh.threads), cols, s, a); };
     const bool ring = M == kSingle ? starts : pieces;
