@@ -80,7 +80,8 @@ __device__ __forceinline__ float reciprocal(float v) {
 // sqrt(v) rounded to nearest for 2^-100 <= v < inf, without the library's
 // branch for the other values: with y near 1 / sqrt(v) and s = v y, the residual
 // v - s s is exact in one FMA and s + (v - s s) y / 2 rounds correctly
-// (Markstein's correction step; compared with sqrtf for every float of that range).
+// (Markstein's correction step; tests/test_gpu_adamw_root.py compares the scales
+// that come of it for every mantissa under an even and an odd exponent).
 constexpr float kRootLow = 0x1p-100f;
 __device__ __forceinline__ float root_in_range(float v) {
   float y;
