@@ -430,10 +430,12 @@ moe_status moe_aux_coef_next(float coef, float drop_rate, float beta, float xi, 
  * moe_layer_norm_backward: the gradients of <dy, y> + <dsum, h> with respect
  *   to h (which are those of x and of add), gamma and beta.
  *   dy[rows, d]; x[rows, d]: h of the forward (its sum when add was given);
- *   mean, rstd: from the forward; gamma or NULL; dsum[rows, d] or NULL: the
- *   gradient that reaches h past the norm; dx[rows, d] (may be dsum itself, or
- *   dy when dy_dtype is dx_dtype); dgamma[d], dbeta[d] fp32 or NULL, fully written
- *   (zeros when rows is 0), summed in a fixed order.
+ *   mean, rstd: from the forward, their product inside fp32's range (it is not
+ *   for a constant row above some 1e36, whose dx may be NaN); gamma or NULL;
+ *   dsum[rows, d] or NULL: the gradient that reaches h past the norm;
+ *   dx[rows, d] (may be dsum itself, or dy when dy_dtype is dx_dtype);
+ *   dgamma[d], dbeta[d] fp32 or NULL, fully written (zeros when rows is 0),
+ *   summed in a fixed order.
  *   stats: device moe_stats or NULL; a bounded wait that gave up sets
  *   MOE_DEV_TIMEOUT in status.  With or without stats, dx of the rows that it
  *   missed, dgamma and dbeta are NaN then.

@@ -12,10 +12,11 @@
 // gets the NaN code and leaves its block's scale alone.
 //
 // 12 to 30 bytes an element are the floor.  32-bit states reach it (67 M
-// elements with master copies: 326 us, 6.2 TB/s); with 8-bit states some 45
+// elements with master copies: 326 us, 6.2 TB/s); with 8-bit states some 51
 // instructions an element (two conversions each way, a root, a reciprocal, two
 // maxima) take as long as the 12 bytes, and the kernel is bound by issue as
-// much as by memory (0.55 G elements: 1175 us, 5.7 TB/s).  Hence few
+// much as by memory (0.55 G elements: 1185 us, 5.6 TB/s; 69 M in 5 tensors 153
+// us, in 160 tensors 181, a quarter more instructions).  Hence few
 // instructions: see root_in_range, the common path of encode, and the types
 // taken out of the loop.  m and v are computed in separately rounded steps (no
 // contraction), so that a code does not depend on how a compiler fuses them.
@@ -450,7 +451,8 @@ adamw_kernel(const __grid_constant__ Table<CAP> tab, int ntensors, unsigned ntil
     };
     if (e.bits == 8) {
       // The arithmetic of 8-bit states is near the bytes' time: fp32 gradients (the layer's) of bf16 or fp16
-      // weights without a master copy get code without decisions on types (1143 us where it takes 1290).
+      // weights without a master copy get code without decisions on types (0.55 G elements: 1186 us where it takes
+      // 1305; 69 M in 160 tensors: 181 and 193).
       Entry f = e;
       const bool plain = e.gdt == MOE_DTYPE_F32 && e.master == nullptr;
       if (plain) f.gdt = MOE_DTYPE_F32, f.master = nullptr;
@@ -498,7 +500,7 @@ cudaError_t launch_adamw(const moe_adamw_tensor* t, int nt, const moe_adamw_hype
   h.grad_scale = grad_scale;
   h.state = state;
   constexpr size_t kSmem = (size_t)kStages * kStageBytes * (kThreads / 32);
-  static thread_local Table<kMaxEntries> tab, packed;   // 28 KB each: off the caller's stack
+  static thread_local Table<kMaxEntries> tab, packed;   // 25 KB each: off the caller's stack
   int i = 0;
   do {   // at least one launch: a step over nothing counts, too
     int ne = 0;

@@ -32,8 +32,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kLossBlocksPerSm = 2;   // by their registers: up to 128 with 16 experts a lane
 constexpr int kMaxLossBlocks = 1024;
-// One block does it all up to here: 7 us for 16 x 8, 11.4 us for 256 x 64, where three kernels take 9.5 us but
-// another 5 us of launching.
+// One block does it all up to here: 4.2 to 6.9 us in a graph for 16 x 8 to 512 x 16 and 32 x 256, where three
+// kernels take 6.4 to 7.7; calls in a row take 8 and 11.4.  Above, three kernels win in a graph: 256 x 64 8.9 and
+// 7.8, 1024 x 16 11.4 and 6.8.
 constexpr int kSmallScores = 8192, kSmallTokens = 512;
 
 // Words at the start of the workspace; n_s of every sequence follows.
