@@ -44,3 +44,16 @@ def test_statistics_of_infinite_sums(d, x, many):
     within(y[fine], ry, tol, "y")
     within(mu[fine], rmu, e_mu + 2.0 ** -24 * np.abs(rmu), "mean")
     within(rs[fine], rrs, e_rs + 2.0 ** -22 * rrs, "rstd")
+
+
+@pytest.mark.parametrize("eps", [1.4e-45, 4.2e-45, 1e-44, 1e-40, 1e-38, 1e-5, 1e30])
+def test_rstd_of_constant_rows_is_the_root_of_eps(eps):
+    """Subnormal eps among them; each rstd to the few roundings of the root."""
+    eps = float(np.float32(eps))
+    cfg = moe.make_norm_config(5, 96, eps, x="f32")
+    X, Y = torch.full((5, 96), 0.75, device="cuda"), torch.empty(5, 96, device="cuda")
+    mean, rstd = torch.empty(5, device="cuda"), torch.empty(5, device="cuda")
+    moe.moe_layer_norm_forward(cfg, X, None, None, Y, mean=mean, rstd=rstd)
+    torch.cuda.synchronize()
+    assert bool((mean == 0.75).all()) and not Y.any()
+    within(rstd, np.full(5, eps ** -0.5), 8 * 2.0 ** -24 * eps ** -0.5, "rstd")
