@@ -190,6 +190,7 @@ __device__ __forceinline__ float reciprocal(float x) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kFarBelow = 0x1p-28f;   // a sum of sigmoids
 
 // How the experts of a token lie in its lanes, 4 N each: kSingle strided by the
 // lanes, kVector in quads of consecutive ones, kWhole the same without a gap.
@@ -201,9 +202,9 @@ enum Mode { kSingle, kVector, kWhole };
 //
 // Softmax: e = exp(z - max).  Sigmoid: with x = exp(-|z|) and r = 1 / (1 + x),
 // sigmoid = r or x r by z's sign and its slope sigmoid (1 - sigmoid) = x r r,
-// without a maximum; where all scores are so far below zero that their sum
-// leaves fp32's range, exp(z - max) again (sigmoid is exp there to the last
-// bit).  ex2.approx on z log2(e) adds a few units in the last place and
+// without a maximum; where all scores are so far below zero that the small ones
+// among them would leave fp32's range before their shares do, exp(z - max)
+// again (sigmoid is exp there to 2^-28).  ex2.approx on z log2(e) adds a few units in the last place and
 // |z| / 2^24, relative.
 // DT: the scores' type, known here so that no element asks for it.
 template <int N, Mode M, bool SIGMOID, int DT>
@@ -334,7 +335,7 @@ __device__ __forceinline__ float loss_of_run(const Loss& a, int run, int end) {
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
         dot += __shfl_xor_sync(0xffffffffu, dot, o);
       });
-      if (SIGMOID && __any_sync(0xffffffffu, used && sum < 0x1p-80f)) {   // all scores of some token below -55
+      if (SIGMOID && __any_sync(0xffffffffu, used && sum < kFarBelow)) {   // all scores of some token below -19
         const float sum0 = sum, dot0 = dot;
         float g0[N][4];
 #pragma unroll
@@ -347,7 +348,7 @@ __device__ __forceinline__ float loss_of_run(const Loss& a, int run, int end) {
           sum += __shfl_xor_sync(0xffffffffu, sum, o);
           dot += __shfl_xor_sync(0xffffffffu, dot, o);
         });
-        if (!(sum0 < 0x1p-80f)) {   // this group's token was fine
+        if (!(sum0 < kFarBelow)) {   // this group's token was fine
           sum = sum0, dot = dot0;
 #pragma unroll
           for (int q = 0; q < N; ++q)
